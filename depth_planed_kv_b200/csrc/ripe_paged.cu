@@ -1,0 +1,370 @@
+// ripe_paged.cu -- the paged cache beside the tensor-core attention kernels: the write
+// of new tokens (ripe_paged_append), the attention of chunks in 32 bits or at head sizes
+// the tensor-core kernels have no form for, and the kernel that joins cut items.
+#include <math.h>
+
+#include "ripe_launch.h"
+#include "ripe_paged.cuh"
+#include "ripe_paged_launch.h"
+#include "sm100_ptx.cuh"
+
+using namespace sm100;
+
+namespace {
+
+// ------------------------------------------------------------------ append
+// Row r of K and V goes to slot pos % page of page table[seq][pos / page], pos = ctx +
+// r - row0[seq].  A copy: bound by HBM (read once, written once).  One block per row and
+// share of its 16-byte vectors; the row's sequence comes from a 32-way search of row0
+// (two rounds of loads by one warp; 1024 sequences at most).
+constexpr int kAppendThreads = 128, kAppendVecs = 4;
+
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ PagedArgs a,
+                                                                      const char* __restrict__ K,
+                                                                      const char* __restrict__ V, int64_t row_stride,
+                                                                      int esize) {
+    const int64_t row = blockIdx.x;
+    __shared__ int64_t s_off;  // elements from the pages' base to the token's head 0, or -1
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, per = (a.nseq + 31) / 32;
+        // the last sequence with row0 <= row
+        const int i = min(lane * per, a.nseq);
+        const unsigned c = __ballot_sync(0xffffffffu, i < a.nseq && __ldg(a.row0 + i) <= row);
+        const int lo = c ? (31 - __clz(c)) * per : 0;
+        const int j = lo + lane;
+        const unsigned f = __ballot_sync(0xffffffffu, lane < per && j < a.nseq && __ldg(a.row0 + j) <= row);
+        const int seq = f ? lo + 31 - __clz(f) : -1;
+        if (lane == 0) {
+            int64_t off = -1;
+            if (seq >= 0) {
+                const int r0 = __ldg(a.row0 + seq), e = __ldg(a.row0 + seq + 1), ctx = __ldg(a.ctx + seq);
+                if (r0 < 0 || e < r0 || e > a.nrows) {
+                    if (a.err) set_device_error(a.err, RIPE_DEVERR_ROWS);
+                } else if (row < e) {
+                    const int64_t pos = ctx + (row - r0);
+                    if (ctx < 0 || ctx + (int64_t)(e - r0) > (int64_t)a.table_width * a.page) {
+                        if (a.err) set_device_error(a.err, RIPE_DEVERR_CAPACITY);
+                    } else {
+                        const int id = __ldg(a.table + seq * a.table_stride + pos / a.page);
+                        if (id < 0 || id >= a.npages) {
+                            if (a.err) set_device_error(a.err, RIPE_DEVERR_PAGE);
+                        } else {
+                            off = id * a.page_stride + (pos % a.page) * a.pos_stride;
+                        }
+                    }
+                }
+            }
+            s_off = off;
+        }
+    }
+    __syncthreads();
+    const int64_t off = s_off;
+    if (off < 0) return;
+    const int per_head = a.d * esize / 16, total = a.Hkv * per_head;
+    const uint4* src[2] = {reinterpret_cast<const uint4*>(K + row * row_stride * esize),
+                           reinterpret_cast<const uint4*>(V + row * row_stride * esize)};
+    char* dst[2] = {const_cast<char*>(a.k) + off * esize, const_cast<char*>(a.v) + off * esize};
+    uint4 x[2][kAppendVecs];
+    const int i0 = blockIdx.y * kAppendThreads * kAppendVecs + threadIdx.x;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int j = 0; j < kAppendVecs; ++j) {
+            const int i = i0 + j * kAppendThreads;
+            if (i < total) x[kv][j] = __ldcs(src[kv] + i);
+        }
+#pragma unroll
+    for (int j = 0; j < kAppendVecs; ++j) {
+        const int i = i0 + j * kAppendThreads;
+        if (i >= total) break;
+        const int h = i / per_head;
+        const int64_t at = h * a.head_stride * esize + (int64_t)(i - h * per_head) * 16;
+        *reinterpret_cast<uint4*>(dst[0] + at) = x[0][j];
+        *reinterpret_cast<uint4*>(dst[1] + at) = x[1][j];
+    }
+}
+
+// ------------------------------------------------------------------ attention on CUDA cores
+// Items of 16 rows (tokens x heads of the group), 32 keys at a time, double-buffered in
+// shared memory by cp.async as they lie in the cache; fp32 arithmetic (FFMA).  Eight
+// lanes share a row: four of the 32 scores each, then d/8 channels of O each.
+constexpr int kSimtThreads = 128, kRows = 16, kKT = 32;
+constexpr int kSimtMinCost = 4;
+
+template <typename Elem>
+__device__ __forceinline__ float4 load4(const char* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const char* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const char* p) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u), __uint_as_float(x.y << 16),
+                       __uint_as_float(x.y & 0xFFFF0000u));
+}
+
+// Shared-memory row pitch: 16 bytes more than the row, so that eight rows' vectors at one
+// channel fall into different banks.
+__host__ __device__ inline int simt_pitch(int d, int esize) { return d * esize + 16; }
+
+template <typename Elem>
+__global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_constant__ PagedArgs a) {
+    constexpr int ES = sizeof(Elem);
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float s_p[kRows][kKT + 1];
+    const int pitch = simt_pitch(a.d, ES), tile = kKT * pitch;
+    char* sQ = smem;                 // [16] rows
+    char* sKV = smem + kRows * pitch;  // [2 buffers][K, V][32] rows
+    const int tid = threadIdx.x, row = tid / 8, sub = tid % 8;
+    const int nv = a.d * ES / 16, n4 = a.d / 4;
+
+    if (tid == 0) a.hdr[blockIdx.x].kind = 0;
+    PagedPlan<kKT> plan;
+    plan.template begin<kSimtThreads>(a, *reinterpret_cast<PagedPlanSmem*>(smem), kSimtMinCost);
+    PagedSeg s;
+    while (plan.next(a, s)) {
+        const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1, rows = s.ntok * a.G;
+        const int tok = row / a.G, pos = p0 + tok;
+        const bool valid = row < rows;
+        __syncthreads();  // the previous item's tiles and Q are no longer read
+        for (int i = tid; i < kRows * nv; i += kSimtThreads) {
+            const int r = i / nv, v = i - r * nv, tk = r / a.G;
+            const bool on = r < rows;
+            cp_async16_zfill(sQ + r * pitch + v * 16,
+                             a.q + (on ? ((s.r + s.t0 + tk) * a.q_rs + (int64_t)(s.head * a.G + r - tk * a.G) * a.d) * ES + v * 16
+                                       : 0),
+                             on);
+        }
+        auto load = [&](int t, int b) {
+            const int k0 = s.tiles.tile(t) * kKT;
+            char* dk = sKV + b * 2 * tile;
+            for (int i = tid; i < kKT * nv; i += kSimtThreads) {
+                const int r = i / nv, v = i - r * nv, key = k0 + r;
+                const bool on = key <= p1;  // later slots hold anything: read as zeros
+                const int64_t off = on ? (paged_page(a, s.seq, key) * a.page_stride + s.head * a.head_stride +
+                                          (key % a.page) * a.pos_stride) * ES + v * 16
+                                       : 0;
+                cp_async16_zfill(dk + r * pitch + v * 16, a.k + off, on);
+                cp_async16_zfill(dk + tile + r * pitch + v * 16, a.v + off, on);
+            }
+            cp_async_commit();
+        };
+        float m = -INFINITY, l = 0.f;
+        float4 o[4];  // channels 4 (sub + 8 j)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        load(s.ta, 0);
+        for (int t = s.ta; t < s.tb; ++t) {
+            const int b = (t - s.ta) & 1, k0 = s.tiles.tile(t) * kKT;
+            if (t + 1 < s.tb) {
+                load(t + 1, b ^ 1);
+                cp_async_wait_group<1>();
+            } else {
+                cp_async_wait_group<0>();
+            }
+            __syncthreads();
+            const char* K = sKV + b * 2 * tile;
+            const char* V = K + tile;
+            const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < n4; ++i) {
+                const float4 q = load4<Elem>(sQ + row * pitch + i * 4 * ES);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 k = load4<Elem>(K + (sub + 8 * j) * pitch + i * 4 * ES);
+                    sc[j] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, sc[j]))));
+                }
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sc[j] = part && !paged_seen(a, k0 + sub + 8 * j, pos) ? -INFINITY : sc[j] * a.scale_log2;
+                mx = fmaxf(mx, sc[j]);
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m, mx), f = m == mn ? 1.f : exp2f(m - mn), ref = mn == -INFINITY ? 0.f : mn;
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j].x *= f;
+                o[j].y *= f;
+                o[j].z *= f;
+                o[j].w *= f;
+                const float e = exp2f(sc[j] - ref);
+                l += e;
+                s_p[row][sub + 8 * j] = e;
+            }
+            __syncwarp();  // a row's eight lanes sit in one warp
+            auto add = [&](int key) {
+                const float p = s_p[row][key];
+                if (part && p == 0.f) return;  // a hidden key's value may be anything
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (sub + 8 * j < n4) {
+                        const float4 v = load4<Elem>(V + key * pitch + (sub + 8 * j) * 4 * ES);
+                        o[j].x = fmaf(p, v.x, o[j].x);
+                        o[j].y = fmaf(p, v.y, o[j].y);
+                        o[j].z = fmaf(p, v.z, o[j].z);
+                        o[j].w = fmaf(p, v.w, o[j].w);
+                    }
+                }
+            };
+            for (int key = 0; key < kKT; ++key) add(key);
+            __syncthreads();  // before the next load into this buffer
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const bool whole = paged_whole(s);
+        if (tid == 0 && !whole && s.ta > 0) {
+            PagedHdr h;
+            h.kind = s.tb == s.tiles.nt ? 2 : 1;
+            h.row0 = s.r + s.t0;
+            h.ntok = s.ntok;
+            h.head = s.head;
+            a.hdr[blockIdx.x] = h;
+        }
+        if (!valid) continue;
+        const int64_t orow = s.r + s.t0 + tok;
+        const int head = s.head * a.G + row - tok * a.G;
+        float* part = paged_slot(a, blockIdx.x, s.ta > 0 ? 0 : 1);
+        if (sub == 0) {
+            if (!whole) {
+                part[row] = m;
+                part[a.slot_rows + row] = l;
+            } else if (a.lse) {
+                a.lse[orow * a.H + head] = m * 0.693147180559945309f + logf(l);
+            }
+        }
+        const float inv = whole ? 1.f / l : 1.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (sub + 8 * j >= n4) break;
+            const int c = 4 * (sub + 8 * j);
+            if (!whole) {
+                float2* dst = reinterpret_cast<float2*>(part + 2 * a.slot_rows + row * a.d + c);
+                dst[0] = make_float2(o[j].x, o[j].y);
+                dst[1] = make_float2(o[j].z, o[j].w);
+            } else if constexpr (ES == 4) {
+                *reinterpret_cast<float4*>(a.o + (orow * a.o_rs + (int64_t)head * a.d + c) * 4) =
+                    make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
+            } else {
+                *reinterpret_cast<uint2*>(a.o + (orow * a.o_rs + (int64_t)head * a.d + c) * 2) =
+                    make_uint2(pack_bf16(o[j].x * inv, o[j].y * inv), pack_bf16(o[j].z * inv, o[j].w * inv));
+            }
+        }
+    }
+    grid_launch_dependents();
+}
+
+// ------------------------------------------------------------------ merge
+// One block column per CTA of the attention kernel; a CTA that ended an item it did not
+// begin joins that item's partials, from the CTA that began it (its slot B) over the ones
+// in the middle to itself (slot A):
+//   m = max m_k, l = sum 2^(m_k - m) l_k, O = sum 2^(m_k - m) O_k / l.
+// A warp per row, its lanes over channel pairs.  Bound by L2 latency: the partials were
+// written just before.
+constexpr int kMergeWarps = 4, kMergeThreads = 32 * kMergeWarps;
+
+template <typename Elem>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedArgs a) {
+    grid_dependency_wait();
+    const int c1 = blockIdx.x;
+    const PagedHdr h = a.hdr[c1];
+    if (h.kind != 2) return;
+    int c0 = c1 - 1;
+    while (c0 > 0 && a.hdr[c0].kind == 1) --c0;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int stride = a.slot_rows * (a.d + 2);
+    // Rows of the item as its kernel numbered them: the tensor-memory kernel leaves the
+    // rows of an M tile past its last token empty.
+    const int per = a.tok1 * a.G, gap = a.tpt > a.tok1 ? 128 - per : 0, rows = h.ntok * a.G;
+    for (int i = blockIdx.y * kMergeWarps + warp; i < rows; i += gridDim.y * kMergeWarps) {
+        const int row = i < per ? i : i + gap;
+        const float* first = paged_slot(a, c0, 1);
+        const float* rest = paged_slot(a, c0 + 1, 0);
+        const int n = c1 - c0;  // partials after the first
+        float m = first[row];
+        for (int k = lane; k < n; k += 32) m = fmaxf(m, rest[(int64_t)k * 2 * stride + row]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+        const int np = a.d / 2;
+        for (int k = 0; k <= n; ++k) {
+            const float* p = k == 0 ? first : rest + (int64_t)(k - 1) * 2 * stride;
+            const float mk = p[row], f = mk == m ? 1.f : exp2f(mk - m);
+            l += f * p[a.slot_rows + row];
+            const float2* v = reinterpret_cast<const float2*>(p + 2 * a.slot_rows + row * a.d);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (lane + 32 * j < np) {
+                    const float2 x = v[lane + 32 * j];
+                    o[2 * j] += f * x.x;
+                    o[2 * j + 1] += f * x.y;
+                }
+        }
+        const int tok = i / a.G, head = h.head * a.G + i - tok * a.G;
+        const int64_t orow = h.row0 + tok;
+        if (lane == 0 && a.lse) a.lse[orow * a.H + head] = m * 0.693147180559945309f + logf(l);
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (lane + 32 * j < np) {
+                char* dst = a.o + (orow * a.o_rs + (int64_t)head * a.d + 2 * (lane + 32 * j)) * sizeof(Elem);
+                if constexpr (sizeof(Elem) == 4)
+                    *reinterpret_cast<float2*>(dst) = make_float2(o[2 * j] * inv, o[2 * j + 1] * inv);
+                else
+                    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[2 * j] * inv, o[2 * j + 1] * inv);
+            }
+    }
+}
+
+template <typename Elem>
+cudaError_t simt_t(const PagedArgs& a, int grid, cudaStream_t st) {
+    static PerDeviceOnce once;
+    const int smem = (kRows + 4 * kKT) * simt_pitch(a.d, sizeof(Elem));
+    cudaError_t e = per_device_once(once, [] {
+        return cudaFuncSetAttribute(paged_simt_kernel<Elem>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (kRows + 4 * kKT) * simt_pitch(128, sizeof(Elem)));
+    });
+    if (e != cudaSuccess) return e;
+    // the plan's arrays share the tiles' memory
+    paged_simt_kernel<Elem><<<grid, kSimtThreads, smem > (int)sizeof(PagedPlanSmem) ? smem : (int)sizeof(PagedPlanSmem), st>>>(a);
+    ripe_count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_simt(PagedArgs a, int dtype, int grid, cudaStream_t st) {
+    return dtype == RIPE_F32 ? simt_t<float>(a, grid, st) : simt_t<__nv_bfloat16>(a, grid, st);
+}
+
+cudaError_t launch_paged_merge(const PagedArgs& a, int dtype, int grid, cudaStream_t st) {
+    const int most = a.tpt < a.max_ntok ? a.tpt : a.max_ntok;
+    int y = (most * a.G + kMergeWarps - 1) / kMergeWarps;
+    y = y < 1 ? 1 : y > 16 ? 16 : y;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)y);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    ripe_count_launch();
+    return dtype == RIPE_F32 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<float>, a)
+                             : cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, a);
+}
+
+cudaError_t launch_paged_append(const PagedArgs& a, const char* K, const char* V, int64_t row_stride, int esize,
+                                cudaStream_t st) {
+    const int vecs = a.Hkv * a.d * esize / 16, per = kAppendThreads * kAppendVecs;
+    paged_append_kernel<<<dim3((unsigned)a.nrows, (unsigned)((vecs + per - 1) / per)), kAppendThreads, 0, st>>>(
+        a, K, V, row_stride, esize);
+    ripe_count_launch();
+    return cudaGetLastError();
+}

@@ -1,0 +1,309 @@
+// ripe_paged.cuh -- argument block and device-side work plan shared by the kernels
+// of ripe_paged_attn (attention of chunks of new tokens over a paged cache).
+//
+// Work.  The new tokens of a sequence are cut into row tiles of `tpt` tokens; a row
+// tile and one key/value head are an item, whose rows are (token, query head of the
+// group).  An item's keys are cut into tiles of KT; those no row can see (past the
+// last token, or behind the window and past the first `sinks` tokens) are left out.
+// An item costs its key tiles times its M tiles.  All items of the call, in the
+// order (sequence, row tile, head), form one line of that cost, and each CTA takes an
+// equal stretch of it, whatever the mix of lengths: the lengths are on the device
+// only, so each CTA finds its own stretch from ctx_len and row0 (two block-wide
+// scans, about 2 us).  An item inside one stretch is finished by its CTA; one that
+// is cut leaves partials (m, l, unnormalised O) for paged_merge_kernel, at most two
+// per CTA: the item its stretch begins inside (slot A), and the one it ends inside
+// (slot B).  The order of the merge follows the CTA numbers, so results repeat bit
+// for bit.
+#pragma once
+
+#include <stdint.h>
+
+#include "ripe_internal.cuh"
+
+constexpr int kPagedMaxSeqs = 1024;
+
+// What a CTA left in its slot A: 0 nothing, 1 a middle stretch of an item, 2 the end
+// of an item (then the item follows).
+struct PagedHdr {
+    int kind, row0, ntok, head, pad[4];
+};
+
+struct PagedArgs {
+    const char *q, *k, *v;
+    char* o;
+    float* lse;
+    int64_t q_rs, o_rs;                           // elements between tokens' rows
+    int64_t page_stride, head_stride, pos_stride;  // elements
+    const int32_t *table, *ctx, *row0;
+    int64_t table_stride;
+    int table_width, nseq, nrows, H, Hkv, G, d, page, npages;
+    int window, sinks;  // window 0: none
+    int max_ntok;       // longer sequences are skipped
+    int tok1, tpt;      // tokens of one M tile and of one row tile (1 or 2 M tiles)
+    float scale_log2;
+    float* part;        // [CTA][2] slots of slot_rows x (d + 2) floats
+    PagedHdr* hdr;      // [CTA]
+    int slot_rows;
+    int32_t* err;       // never NULL
+};
+
+// The chunk of sequence i: `n` tokens behind `c` cached ones, rows from `r`.  n = 0
+// for a sequence that is skipped (bad offsets, or past its pages).
+struct PagedSeq {
+    int c, n, r;
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int i, bool report) {
+    PagedSeq s;
+    s.r = __ldg(a.row0 + i);
+    s.c = __ldg(a.ctx + i);
+    const int e = __ldg(a.row0 + i + 1);
+    s.n = 0;
+    if (s.r < 0 || e < s.r || e > a.nrows || e - s.r > a.max_ntok) {
+        if (report) set_device_error(a.err, RIPE_DEVERR_ROWS);
+    } else if (s.c < 0 || (int64_t)s.c + (e - s.r) > (int64_t)a.table_width * a.page) {
+        if (report) set_device_error(a.err, RIPE_DEVERR_CAPACITY);
+    } else {
+        s.n = e - s.r;
+    }
+    return s;
+}
+
+// Key tiles of tokens [t0, t0 + nt) of a chunk: tiles [0, ts) hold the first tokens,
+// then tiles from `tlo` on (the same line where the two meet).
+struct PagedTiles {
+    int nt, ts, tlo;
+    __device__ __forceinline__ int tile(int t) const { return t < ts ? t : t - ts + tlo; }
+};
+
+template <int KT>
+__device__ __forceinline__ PagedTiles paged_tiles(const PagedArgs& a, int c, int t0, int ntok) {
+    PagedTiles p;
+    const int p0 = c + t0, hi = p0 + ntok;
+    p.nt = (hi + KT - 1) / KT;
+    p.ts = 0;
+    p.tlo = 0;
+    if (a.window > 0 && a.window <= p0) {
+        const int lo = (p0 + 1 - a.window) / KT, ts = (min(a.sinks, hi) + KT - 1) / KT;
+        if (ts < lo) {
+            p.nt += ts - lo;
+            p.ts = ts;
+            p.tlo = lo;
+        }
+    }
+    return p;
+}
+
+// Every key of [k0, k0 + nk) is seen by every token of positions [p0, p1].
+__device__ __forceinline__ bool paged_all_seen(const PagedArgs& a, int k0, int nk, int p0, int p1) {
+    return k0 + nk - 1 <= p0 && (a.window <= 0 || k0 > p1 - a.window || k0 + nk <= a.sinks);
+}
+// Some key of [k0, k0 + nk) may be seen by some token of positions [p0, p1].
+__device__ __forceinline__ bool paged_any_seen(const PagedArgs& a, int k0, int nk, int p0, int p1) {
+    return k0 <= p1 && (a.window <= 0 || k0 + nk - 1 > p0 - a.window || k0 < a.sinks);
+}
+__device__ __forceinline__ bool paged_seen(const PagedArgs& a, int key, int pos) {
+    return key <= pos && (a.window <= 0 || key > pos - a.window || key < a.sinks);
+}
+
+// Page of key `key` of sequence `seq`: an id outside the pool is reported and read as
+// page 0 (that sequence's rows then mean nothing).
+__device__ __forceinline__ int paged_page(const PagedArgs& a, int seq, int key) {
+    int id = __ldg(a.table + seq * a.table_stride + key / a.page);
+    if (id < 0 || id >= a.npages) {
+        set_device_error(a.err, RIPE_DEVERR_PAGE);
+        id = 0;
+    }
+    return id;
+}
+
+// A stretch of one item: key tiles [ta, tb) of its `nt`.
+struct PagedSeg {
+    int seq, c, r, n;       // the sequence (PagedSeq)
+    int t0, ntok, head, w;  // the row tile's tokens, the key/value head, M tiles
+    int ta, tb;
+    PagedTiles tiles;
+};
+
+struct PagedPlanSmem {
+    int sq[kPagedMaxSeqs + 1];  // row tiles before each sequence
+    int64_t tp[512 + 1];        // cost before each thread's run of row tiles (one head)
+    int64_t warp[16];
+};
+
+// Inclusive block-wide scan of one value per thread (all threads call it).
+template <typename T>
+__device__ __forceinline__ T paged_scan(T v, T* warp_sums) {
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[w] = v;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) v += warp_sums[i];
+    return v;
+}
+
+template <int KT>
+struct PagedPlan {
+    int64_t x, x_end;  // this CTA's stretch of the line (x moves)
+    int qt;            // row tile within the sequence
+    int off;           // cost already behind x within the item
+    PagedSeg s;        // the current item (s.head included)
+
+    __device__ __forceinline__ int item(const PagedArgs& a) {  // s.seq, qt -> the row tile; its cost
+        s.t0 = qt * a.tpt;
+        s.ntok = min(a.tpt, s.n - s.t0);
+        s.w = s.ntok > a.tok1 ? 2 : 1;
+        s.tiles = paged_tiles<KT>(a, s.c, s.t0, s.ntok);
+        return s.tiles.nt * s.w;
+    }
+    __device__ __forceinline__ void load(const PagedArgs& a, int i) {
+        const PagedSeq q = paged_seq(a, i, false);
+        s.seq = i;
+        s.c = q.c;
+        s.n = q.n;
+        s.r = q.r;
+    }
+
+    // All threads of the block; `sm` may be reused after the call (it ends with a barrier).
+    template <int THREADS>
+    __device__ void begin(const PagedArgs& a, PagedPlanSmem& sm, int min_cost) {
+        static_assert(THREADS <= 512, "one run of row tiles per thread");
+        const int tid = threadIdx.x;
+        // row tiles before each sequence
+        int base = 0;
+        for (int i0 = 0; i0 < a.nseq; i0 += THREADS) {
+            const int i = i0 + tid;
+            int nq = 0;
+            if (i < a.nseq) nq = (paged_seq(a, i, blockIdx.x == 0).n + a.tpt - 1) / a.tpt;
+            const int incl = base + paged_scan(nq, reinterpret_cast<int*>(sm.warp));
+            if (i < a.nseq) sm.sq[i + 1] = incl;
+            if (tid == THREADS - 1) sm.warp[15] = incl;  // THREADS / 32 <= 15, or the same value
+            __syncthreads();
+            base = (int)sm.warp[15];
+        }
+        if (tid == 0) sm.sq[0] = 0;
+        __syncthreads();
+        // cost of each thread's run of row tiles
+        const int per = (base + THREADS - 1) / THREADS;
+        const int q0 = min(base, tid * per), q1 = min(base, q0 + per);
+        int64_t cost = 0;
+        if (q0 < q1) {
+            find(a, sm, q0);
+            for (int q = q0; q < q1; ++q) {
+                cost += item(a);
+                step(a);
+            }
+        }
+        const int64_t incl = paged_scan(cost, sm.warp);
+        sm.tp[tid + 1] = incl;
+        if (tid == 0) sm.tp[0] = 0;
+        __syncthreads();
+        const int64_t total = sm.tp[THREADS] * a.Hkv;
+        int64_t len = (total + gridDim.x - 1) / gridDim.x;
+        len = len < min_cost ? min_cost : len;
+        x = len * blockIdx.x;
+        x_end = x + len < total ? x + len : total;
+        if (x < x_end) {
+            const int64_t y = x / a.Hkv;
+            int lo = 0, hi = THREADS;  // the last run with tp <= y
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (sm.tp[mid] <= y) lo = mid; else hi = mid;
+            }
+            int64_t p = sm.tp[lo];
+            find(a, sm, lo * per);
+            int c = item(a);
+            while (p + c <= y) {
+                p += c;
+                step(a);
+                c = item(a);
+            }
+            const int64_t rem = x - p * a.Hkv;
+            s.head = (int)(rem / c);
+            off = (int)(rem % c);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // asynchronous copies may land on `sm` next
+        __syncthreads();
+    }
+    // The sequence and row tile of global row tile q.
+    __device__ __forceinline__ void find(const PagedArgs& a, const PagedPlanSmem& sm, int q) {
+        int lo = 0, hi = a.nseq;  // the last sequence with sq <= q has tiles: sq[lo + 1] > q
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (sm.sq[mid] <= q) lo = mid; else hi = mid;
+        }
+        load(a, lo);
+        qt = q - sm.sq[lo];
+    }
+    // The next row tile (a sequence without tokens has none); stays put after the last.
+    __device__ __forceinline__ void step(const PagedArgs& a) {
+        ++qt;
+        if (qt * (int64_t)a.tpt >= s.n) {
+            int i = s.seq + 1;
+            while (i < a.nseq) {
+                load(a, i);
+                if (s.n > 0) break;
+                ++i;
+            }
+            qt = 0;
+            if (i >= a.nseq) s.n = 0;
+        }
+    }
+
+    // The next stretch of an item; false when the CTA's share is done.
+    __device__ __forceinline__ bool next(const PagedArgs& a, PagedSeg& out) {
+        while (x < x_end) {
+            const int c = item(a);
+            const int64_t room = x_end - x;
+            const int end = (int)(room < c - off ? off + room : c);
+            out = s;
+            out.ta = s.w == 2 ? off >> 1 : off;
+            out.tb = s.w == 2 ? end >> 1 : end;
+            x += end - off;
+            off = 0;
+            if (++s.head == a.Hkv) {
+                s.head = 0;
+                if (x < x_end) step(a);
+            }
+            if (out.tb > out.ta) return true;
+        }
+        return false;
+    }
+};
+
+// Whether a stretch leaves a partial, and where: slot A when it begins inside its
+// item, slot B when it only ends inside.
+__device__ __forceinline__ bool paged_whole(const PagedSeg& s) { return s.ta == 0 && s.tb == s.tiles.nt; }
+
+__device__ __forceinline__ float* paged_slot(const PagedArgs& a, int cta, int slot) {
+    return a.part + ((int64_t)cta * 2 + slot) * a.slot_rows * (a.d + 2);
+}
+// A slot holds m [slot_rows] (log2 units), l [slot_rows], then O [slot_rows][d].
+
+// Adds the values of V that are not finite, of keys the row sees in key tiles that are
+// not seen whole by all rows: the kernels read such values as zeros there, because a
+// matrix product would carry them (0 * inf) into rows whose mask hides them.
+// `o`: `n` channels from channel c0.
+template <int KT>
+__device__ __noinline__ void paged_add_nonfinite(const PagedArgs& a, const PagedSeg& s, int pos, int c0, int n, float* o) {
+    const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1;
+    for (int t = s.ta; t < s.tb; ++t) {
+        const int k0 = s.tiles.tile(t) * KT;
+        if (paged_all_seen(a, k0, KT, p0, p1)) continue;
+        for (int key = k0; key < k0 + KT && key <= pos; ++key) {
+            if (!paged_seen(a, key, pos)) continue;
+            const int64_t row = paged_page(a, s.seq, key) * a.page_stride + s.head * a.head_stride +
+                                (key % a.page) * a.pos_stride;
+            const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v) + row + c0;
+            for (int i = 0; i < n; ++i) {
+                const float f = __bfloat162float(v[i]);
+                if (!isfinite(f)) o[i] += f;
+            }
+        }
+    }
+}

@@ -1,0 +1,511 @@
+// ripe_paged_sm100.cu -- ripe_paged_attn on the tensor cores: chunks of new tokens
+// (prompts, chunks of prompts, draft blocks with many rows) over a paged cache; bf16,
+// head size 64, 96 or 128.
+//
+// Per item (row tile of tokens x the query heads of one key/value head, see
+// ripe_paged.cuh): S = Q K^T and O += P V with the online softmax
+//   m' = max(m, max_k S), P = 2^(c S - m'), l' = l 2^(m - m') + sum P, O' = O 2^(m - m') + P V
+// (c = scale * log2 e).  m moves only when a row's maximum grew by more than 2^8: until
+// then P stays below 2^8, which fp32 sums and bf16's exponent hold without loss, and the
+// accumulator need not be read back.  l sums the unrounded P; P is rounded to bf16 for
+// the second product (2^-8 of a weight at most, below the rounding of O itself).
+//
+// One persistent CTA per SM, 10 warps: two softmax warpgroups (one row per thread), a
+// TMA warp, an MMA warp.  Two streams s = 0, 1, each with its own S and O in tensor
+// memory (S 2 x 128 columns, P over S, O 2 x d columns), keep the tensor pipe busy with
+// one stream's products while the other's softmax runs:
+//   two M tiles (more than 128 rows): stream s is M tile s, both over the same key tile;
+//   one M tile: stream s takes every second key tile, joined at the item's end.
+// Keys and values arrive in 128-key tiles through one ring of shared-memory stages (K
+// and V in turn), one TMA box per page (or 128 rows of it) and 32 channels, 64-byte
+// swizzle.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+#include <string.h>
+
+#include "ripe_launch.h"
+#include "ripe_paged.cuh"
+#include "ripe_paged_launch.h"
+#include "sm100_ptx.cuh"
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kKT = 128;       // keys per tile
+constexpr int kThreads = 320;  // 8 softmax warps, the TMA warp, the MMA warp
+constexpr int kMinCost = 4;    // key tiles x M tiles a CTA takes at least (two key tiles of two M tiles)
+
+struct alignas(64) PagedMaps {
+    CUtensorMap q, k, v;
+};
+
+template <int D, int ST>
+struct Lay {
+    static constexpr int NCH = D / 32;         // 32-channel chunks
+    static constexpr int TILE = NCH * 8192;    // 128 rows of bf16
+    static constexpr int Q = 0;
+    static constexpr int KV = 2 * TILE;
+    static constexpr int BARS = KV + ST * TILE;
+    static constexpr int NBAR = 2 * ST + 2 + 2 + 2 + 2 + 4;
+    static constexpr int ML = BARS + ((NBAR * 8 + 15) / 16) * 16;  // [2][128] (m, l) of stream 1
+    static constexpr int MISC = ML + 2 * 128 * 8;
+    static constexpr int TOTAL = MISC + 64;
+    static_assert(sizeof(PagedPlanSmem) <= (size_t)ST * TILE, "plan arrays over the stages");
+    static_assert(TOTAL + 512 <= 232448, "shared memory of one CTA");
+};
+
+// Waits with the whole warp: true only if every lane saw the phase complete.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+}
+
+// Zeros the values the matrix product must not see in a key tile that some row sees
+// only in part: keys from `end` on (their slots hold anything), and values that are
+// not finite (returns whether there were any; paged_add_nonfinite puts them back where
+// they are seen).  Thread t of 128 takes key t.  With two M tiles both warpgroups clean
+// the tile, each before its own product: what the later one still writes is what the
+// earlier one wrote.
+template <int NCH>
+__device__ __forceinline__ bool clean_values(char* sv, int t, bool past) {
+    bool found = false;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+        uint4* row = reinterpret_cast<uint4*>(sv + c * 8192 + t * 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 x = row[i];
+            if (past) {
+                if (x.x | x.y | x.z | x.w) row[i] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if ((w[j] & 0x7F80u) == 0x7F80u) {
+                    w[j] &= 0xFFFF0000u;
+                    bad = true;
+                }
+                if ((w[j] & 0x7F800000u) == 0x7F800000u) {
+                    w[j] &= 0xFFFFu;
+                    bad = true;
+                }
+            }
+            if (bad) {
+                row[i] = x;
+                found = true;
+            }
+        }
+    }
+    return found;
+}
+
+template <int D, int ST>
+__global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedMaps tm,
+                                                               const __grid_constant__ PagedArgs a) {
+    using L = Lay<D, ST>;
+    constexpr int NCH = L::NCH;
+    extern __shared__ char smem_raw[];
+    char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) & ~(uintptr_t)511);
+    char* sQ = smem + L::Q;
+    char* sKV = smem + L::KV;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
+    uint64_t *kv_full = bars, *kv_empty = bars + ST, *s_full = bars + 2 * ST, *p_full = s_full + 2, *o_full = p_full + 2,
+             *o_free = o_full + 2, *q_full = o_free + 2, *q_free = q_full + 1, *ml_full = q_free + 1, *drain = ml_full + 1;
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::ML);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
+    volatile int* s_bad = reinterpret_cast<volatile int*>(smem + L::MISC + 16);  // [4] item with non-finite values
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(kv_full + i, 1);
+            mbar_init(kv_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 128);
+            mbar_init(o_full + i, 1);
+            mbar_init(o_free + i, 128);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_free, 1);
+        mbar_init(ml_full, 128);
+        mbar_init(drain, 1);
+        fence_barrier_init();
+        *abort_flag = 0;
+        for (int i = 0; i < 4; ++i) s_bad[i] = 0;
+    }
+    if (warp == 9) {
+        tmem_alloc(s_tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &tm.q : lane == 1 ? &tm.k : &tm.v);
+    PagedPlan<kKT> plan;
+    plan.template begin<kThreads>(a, *reinterpret_cast<PagedPlanSmem*>(sKV), kMinCost);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t S_COL[2] = {tmem, tmem + 128}, O_COL[2] = {tmem + 256, tmem + 256 + D};
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ TMA producer
+        // Lane l: box l of a tile, sub-block l / NCH of its keys (a page, or 128 keys of
+        // one), chunk l % NCH.
+        const int pb = a.page < kKT ? a.page : kKT, nsub = kKT / pb;
+        const int sub = lane / NCH, ch = lane % NCH;
+        const uint32_t box = (uint32_t)pb * 64;
+        PagedSeg s;
+        int it = 0, seg = 0;  // stages filled, segments begun
+        bool ok = true;
+        while (ok && plan.next(a, s)) {
+            const int end = s.c + s.t0 + s.ntok;
+            if (seg > 0 && !(ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, a.err))) break;
+            if (lane == 0) {
+                const uint32_t qbox = (uint32_t)a.tok1 * a.G * 64;
+                mbar_expect_tx(q_full, s.w * NCH * qbox);
+                for (int mt = 0; mt < s.w; ++mt)
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_3d(sQ + (mt * NCH + c) * 8192, &tm.q, 32 * c, s.head * a.G, s.r + s.t0 + mt * a.tok1, q_full);
+            }
+            ++seg;
+            auto page_of = [&](int t) {
+                const int key = s.tiles.tile(t) * kKT + sub * pb;
+                return t < s.tb && sub < nsub && key < end ? paged_page(a, s.seq, key) : -1;
+            };
+            int id = page_of(s.ta);
+            for (int t = s.ta; t < s.tb && ok; ++t) {
+                const int next_id = page_of(t + 1);
+                const int k0 = s.tiles.tile(t) * kKT, y = (k0 + sub * pb) % a.page;
+                const int boxes = min(nsub, (end - k0 + pb - 1) / pb) * NCH;
+                for (int kv = 0; kv < 2; ++kv, ++it) {
+                    const int st = it % ST;
+                    if (it >= ST && !(ok = warp_wait(kv_empty + st, ((it / ST) - 1) & 1, abort_flag, a.err))) break;
+                    if (lane == 0) mbar_expect_tx(kv_full + st, boxes * box);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_4d(sKV + st * L::TILE + ch * 8192 + sub * (int)box, kv ? &tm.v : &tm.k, 32 * ch, y, s.head, id,
+                                    kv_full + st);
+                }
+                id = next_id;
+            }
+        }
+        // Every copy has landed before the CTA's shared memory goes away: on the ordinary
+        // way out the MMA warp waited for all of them.
+        if (!ok || *abort_flag) {
+            volatile int no_abort = 0;
+            if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, &no_abort, a.err);
+            for (int i = it > ST ? it - ST : 0; i < it; ++i) mbar_wait(kv_full + i % ST, (i / ST) & 1, &no_abort, a.err);
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t IDESC_QK = idesc_bf16(128, kKT, 0), IDESC_PV = idesc_bf16(128, D, 1);
+            const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
+            PagedSeg s;
+            int base = 0, seg = 0, steps[2] = {0, 0}, uses[2] = {0, 0};  // stages, segments, steps and segments of a stream
+            bool ok = true;
+            while (ok && plan.next(a, s)) {
+                const int T = s.tb - s.ta, U = T * s.w;
+                auto qk = [&](int u) -> bool {
+                    const int st_i = u & 1, i = s.w == 2 ? u >> 1 : u, k = base + 2 * i, st = k % ST;
+                    if ((s.w == 1 || st_i == 0) && !mbar_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err)) return false;
+                    tc_fence_after();
+                    const uint32_t qa = q0 + (s.w == 2 ? st_i : 0) * L::TILE;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t o = (ks >> 1) * 8192 + (ks & 1) * 32;
+                        mma_bf16(S_COL[st_i], smem_desc(qa + o, 16, 512, kLayoutSwizzle64B),
+                                 smem_desc(kv0 + st * L::TILE + o, 16, 512, kLayoutSwizzle64B), IDESC_QK, ks > 0 ? 1u : 0u);
+                    }
+                    mma_commit(s_full + st_i);
+                    if (s.w == 1 || st_i == 1) mma_commit(kv_empty + st);
+                    return true;
+                };
+                if (!(ok = mbar_wait(q_full, seg & 1, abort_flag, a.err))) break;
+                ++seg;
+                for (int u = 0; u < 2 && u < U && ok; ++u) ok = qk(u);
+                if (ok && U <= 2) mma_commit(q_free);
+                for (int u = 0; u < U && ok; ++u) {
+                    const int st_i = u & 1, i = s.w == 2 ? u >> 1 : u, k = base + 2 * i + 1, st = k % ST;
+                    const bool first = u < 2;
+                    if (!(ok = mbar_wait(p_full + st_i, steps[st_i] & 1, abort_flag, a.err))) break;
+                    ++steps[st_i];
+                    if (first) {
+                        if (uses[st_i] > 0 && !(ok = mbar_wait(o_free + st_i, (uses[st_i] - 1) & 1, abort_flag, a.err))) break;
+                        ++uses[st_i];
+                    }
+                    if ((s.w == 1 || st_i == 0) && !(ok = mbar_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < kKT / 16; ++ks)
+                        mma_bf16_ts(O_COL[st_i], S_COL[st_i] + ks * 8,
+                                    smem_desc(kv0 + st * L::TILE + ks * 1024, 8192, 512, kLayoutSwizzle64B), IDESC_PV,
+                                    (!first || ks > 0) ? 1u : 0u);
+                    if (s.w == 1 || st_i == 1) mma_commit(kv_empty + st);
+                    if (u + 2 >= U) mma_commit(o_full + st_i);
+                    if (u + 2 < U) {
+                        ok = qk(u + 2);
+                        if (ok && u + 3 == U) mma_commit(q_free);
+                    }
+                }
+                base += 2 * T;
+            }
+            // Every MMA issued so far has completed before TMEM is released.
+            volatile int no_abort = 0;
+            mma_commit(drain);
+            mbar_wait(drain, 0, &no_abort, a.err);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ softmax and epilogue
+        const int wg = warp / 4, t = threadIdx.x % 128;  // stream; TMEM lane = row of the M tile
+        const uint32_t lane_addr = (uint32_t)((warp % 4) * 32) << 16;
+        const float c2 = a.scale_log2;
+        const int tok = t / a.G, g = t - tok * a.G;
+        PagedSeg s;
+        int base = 0, seg = 0, steps = 0, joins = 0, uses[2] = {0, 0};  // as in the MMA warp
+        if (threadIdx.x == 0) a.hdr[blockIdx.x].kind = 0;
+        bool ok = true;
+        while (ok && plan.next(a, s)) {
+            const int T = s.tb - s.ta;
+            const int mytok = s.t0 + (s.w == 2 ? wg * a.tok1 : 0) + tok;  // this row's token
+            const bool valid = tok < a.tok1 && mytok < s.t0 + s.ntok;
+            const int pos = s.c + mytok;
+            const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1;
+            const int nsteps = s.w == 2 ? T : (T + 1 - wg) / 2;
+            float m = -INFINITY, l = 0.f;
+            for (int n = 0; n < nsteps && ok; ++n, ++steps) {
+                const int i = s.w == 2 ? n : 2 * n + wg;
+                const int k0 = s.tiles.tile(s.ta + i) * kKT;
+                const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
+                if (!(ok = warp_wait(s_full + wg, steps & 1, abort_flag, a.err))) break;
+                tc_fence_after();
+                float v[kKT];
+#pragma unroll
+                for (int c = 0; c < kKT; c += 32) tmem_ld32(S_COL[wg] + lane_addr + c, v + c);
+                tmem_wait_ld();
+                if (part) {
+                    // keys past the row's own position, or neither in its window nor among the first
+                    const int hi = pos - k0, lo = a.window > 0 ? pos - a.window - k0 : -1, first = a.sinks - k0;
+#pragma unroll
+                    for (int c = 0; c < kKT; ++c)
+                        if (c > hi || (c <= lo && c >= first)) v[c] = -INFINITY;
+                }
+                float mx0 = v[0], mx1 = v[1], mx2 = v[2], mx3 = v[3];
+#pragma unroll
+                for (int c = 4; c < kKT; c += 4) {
+                    mx0 = fmaxf(mx0, v[c]);
+                    mx1 = fmaxf(mx1, v[c + 1]);
+                    mx2 = fmaxf(mx2, v[c + 2]);
+                    mx3 = fmaxf(mx3, v[c + 3]);
+                }
+                const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c2;
+                const bool grow = valid && mx > m + 8.f;  // m = -inf: any finite maximum
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float mn = grow ? mx : m;
+                    const float f = m == mn ? 1.f : ex2(m - mn);  // 0 from m = -inf
+                    m = mn;
+                    l *= f;
+                    if (n > 0) {
+                        // The stream's earlier P V are complete: s_full came after them.
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            float o[32];
+                            tmem_ld32(O_COL[wg] + lane_addr + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] *= f;
+                            tmem_st32(O_COL[wg] + lane_addr + c, o);
+                        }
+                    }
+                }
+                const float mref = m == -INFINITY ? 0.f : m;
+                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                for (int c = 0; c < kKT; c += 32) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float e0 = ex2(fmaf(v[c + j], c2, -mref)), e1 = ex2(fmaf(v[c + j + 1], c2, -mref));
+                        const float e2 = ex2(fmaf(v[c + j + 2], c2, -mref)), e3 = ex2(fmaf(v[c + j + 3], c2, -mref));
+                        l0 += e0;
+                        l1 += e1;
+                        l2 += e2;
+                        l3 += e3;
+                        w[j / 2] = pack_bf16(e0, e1);
+                        w[j / 2 + 1] = pack_bf16(e2, e3);
+                    }
+                    tmem_st16(S_COL[wg] + lane_addr + c / 2, w);
+                }
+                l += (l0 + l1) + (l2 + l3);
+                if (part) {
+                    const int k = base + 2 * i + 1, st = k % ST;
+                    if (!(ok = warp_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
+                    if (clean_values<NCH>(sKV + st * L::TILE, t, k0 + t > p1)) {
+                        s_bad[seg & 3] = seg + 1;
+                        __threadfence_block();
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_full + wg);
+            }
+            if (!ok) break;
+            // -------------------------------------------------------- the item's end
+            const bool whole = paged_whole(s);
+            const int slot = s.ta > 0 ? 0 : 1;
+            if (threadIdx.x == 0 && !whole && s.ta > 0) {
+                PagedHdr h;
+                h.kind = s.tb == s.tiles.nt ? 2 : 1;
+                h.row0 = s.r + s.t0;
+                h.ntok = s.ntok;
+                h.head = s.head;
+                a.hdr[blockIdx.x] = h;
+            }
+            float f0 = 1.f, f1 = 0.f;
+            const bool two = s.w == 1 && T > 1;  // both streams hold a part of the one M tile
+            if (two && wg == 1) {
+                s_ml[(joins & 1) * 128 + t] = make_float2(m, l);
+                mbar_arrive(ml_full);
+            }
+            if (s.w == 2 || wg == 0) {
+                if (!(ok = warp_wait(o_full + wg, uses[wg] & 1, abort_flag, a.err))) break;
+                if (two) {
+                    if (!(ok = warp_wait(ml_full, joins & 1, abort_flag, a.err))) break;
+                    if (!(ok = warp_wait(o_full + 1, uses[1] & 1, abort_flag, a.err))) break;
+                    const float2 x = s_ml[(joins & 1) * 128 + t];
+                    const float mn = fmaxf(m, x.x);
+                    f0 = m == mn ? 1.f : ex2(m - mn);
+                    f1 = x.x == mn ? 1.f : ex2(x.x - mn);
+                    m = mn;
+                    l = l * f0 + x.y * f1;
+                }
+                tc_fence_after();
+                const bool bad = s_bad[seg & 3] == seg + 1;
+                const int head = s.head * a.G + g;
+                const int64_t row = s.r + mytok;
+                const int prow = (s.w == 2 ? wg * 128 : 0) + t;
+                float* part = paged_slot(a, blockIdx.x, slot);
+                if (valid && !whole) {
+                    part[prow] = m;
+                    part[a.slot_rows + prow] = l;
+                } else if (valid && a.lse) {
+                    a.lse[row * a.H + head] = (m + log2f(l)) * 0.693147180559945309f;
+                }
+                const float inv = whole ? 1.f / l : 1.f;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(O_COL[wg] + lane_addr + c, o);
+                    if (two) {
+                        float o1[32];
+                        tmem_ld32(O_COL[1] + lane_addr + c, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + o1[j] * f1;
+                    } else {
+                        tmem_wait_ld();
+                    }
+                    if (c + 32 == D) {
+                        tc_fence_before();
+                        mbar_arrive(o_free + wg);
+                        if (two) mbar_arrive(o_free + 1);
+                    }
+                    if (bad && valid) paged_add_nonfinite<kKT>(a, s, pos, c, 32, o);
+                    if (valid && whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.o + (row * a.o_rs + (int64_t)head * D + c) * 2);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            dst[j / 8] = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
+                                                    pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
+                    } else if (valid) {
+                        float2* dst = reinterpret_cast<float2*>(part + 2 * a.slot_rows + (int64_t)prow * D + c);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) dst[j / 2] = make_float2(o[j], o[j + 1]);
+                    }
+                    __syncwarp();
+                }
+            }
+            uses[0] += 1;
+            uses[1] += s.w == 2 || two;
+            joins += two;
+            base += 2 * T;
+            ++seg;
+        }
+    }
+    grid_launch_dependents();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+template <int D, int ST>
+cudaError_t launch(const PagedMaps& tm, const PagedArgs& a, int grid, cudaStream_t st) {
+    static PerDeviceOnce once;
+    constexpr int smem = Lay<D, ST>::TOTAL + 512;
+    cudaError_t e = per_device_once(once, [] {
+        return cudaFuncSetAttribute(paged_tc_kernel<D, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
+    paged_tc_kernel<D, ST><<<grid, kThreads, smem, st>>>(tm, a);
+    ripe_count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Maps of the pages ([pages][heads][positions][d], any strides) in boxes of `rows`
+// positions of one page and head and 32 channels.
+bool paged_kv_map(void* map, const void* base, const PagedArgs& a, int rows) {
+    const auto encode = encode_fn();
+    if (!encode) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.page, (cuuint64_t)a.Hkv, (cuuint64_t)a.npages};
+    const cuuint64_t strides[3] = {(cuuint64_t)a.pos_stride * 2, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
+    const cuuint32_t box[4] = {32, (cuuint32_t)rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return encode(reinterpret_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int paged_tc_slot_rows() { return 256; }
+
+cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st) {
+    PagedMaps tm;
+    const auto encode = encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.H, (cuuint64_t)a.nrows};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.d * 2, (cuuint64_t)a.q_rs * 2};
+    const cuuint32_t box[3] = {32, (cuuint32_t)a.G, (cuuint32_t)a.tok1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (encode(&tm.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<char*>(a.q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const int rows = a.page < kKT ? a.page : kKT;
+    if (!paged_kv_map(&tm.k, a.k, a, rows) || !paged_kv_map(&tm.v, a.v, a, rows)) return cudaErrorInvalidValue;
+    if (a.d == 64) return launch<64, 12>(tm, a, grid, st);
+    if (a.d == 96) return launch<96, 7>(tm, a, grid, st);
+    if (a.d == 128) return launch<128, 5>(tm, a, grid, st);
+    return cudaErrorInvalidValue;
+}

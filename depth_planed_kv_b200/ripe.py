@@ -37,7 +37,7 @@ RIPE_ERR_CAPTURING = 8
 RIPE_BF16 = 0
 RIPE_F32 = 1
 DEVERR_NAMES = {0: "none", 1: "seq_range", 2: "capacity", 3: "count", 4: "ctx", 5: "branch", 6: "timeout",
-                7: "fork"}
+                7: "fork", 8: "rows", 9: "page"}
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -47,6 +47,19 @@ class ripe_branch_t(ctypes.Structure):
     _fields_ = [("seq", ctypes.c_int32), ("depth", ctypes.c_int32), ("ntok", ctypes.c_int32),
                 ("row0", ctypes.c_int32), ("row_stride", ctypes.c_int32),
                 ("reserved", ctypes.c_int32 * 3)]
+
+
+class ripe_pages_t(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("pos_stride", ctypes.c_int64), ("npages", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32 * 3)]
+
+
+class ripe_paged_batch_t(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("ctx_len", ctypes.c_void_p),
+                ("row0", ctypes.c_void_p), ("table_width", ctypes.c_int32), ("nseq", ctypes.c_int32),
+                ("nrows", ctypes.c_int32), ("max_ntok", ctypes.c_int32), ("err_dev", ctypes.c_void_p)]
 
 
 def _sig(name, args, res=ctypes.c_int):
@@ -76,6 +89,10 @@ _sig("ripe_cache_verify_path", [_P, ctypes.POINTER(_I)])
 _sig("ripe_cache_set_all_depths_kernel", [_P, _I])
 _sig("ripe_debug_stall_next_verify", [_P, ctypes.c_longlong])
 _sig("ripe_accept", [_I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P])
+_sig("ripe_paged_append", [_P, _P, _P, _P, ctypes.c_int64, _P])
+_sig("ripe_paged_attn_workspace", [_P, _I, _I, ctypes.POINTER(ctypes.c_size_t)])
+_sig("ripe_paged_attn", [_P, _P, _I, _P, ctypes.c_int64, _I, _I, ctypes.c_float, _P, ctypes.c_int64, _P, _P,
+                         ctypes.c_size_t, _P])
 _sig("ripe_cache_buffers", [_P] + [ctypes.POINTER(_P)] * 7)
 _sig("ripe_read_meta", [_P, _P, _P, _P, _P])
 _sig("ripe_get_device_error", [_P, _P, _P])
@@ -88,6 +105,7 @@ EXPORTED = ["ripe_cache_bytes", "ripe_cache_create", "ripe_cache_destroy", "ripe
             "ripe_verify_attn_all_depths", "ripe_verify_attn_all_depths_sliding", "ripe_verify_attn_noalloc", "ripe_reserve_workspace",
             "ripe_synth_fill", "ripe_cache_verify_path", "ripe_cache_set_all_depths_kernel",
             "ripe_debug_stall_next_verify", "ripe_accept",
+            "ripe_paged_append", "ripe_paged_attn_workspace", "ripe_paged_attn",
             "ripe_cache_buffers", "ripe_read_meta", "ripe_get_device_error", "ripe_launch_count",
             "ripe_error_string", "ripe_last_error"]
 
@@ -141,6 +159,95 @@ def ripe_accept(zp: torch.Tensor, zq: torch.Tensor, zf: Optional[torch.Tensor], 
                             ctypes.c_float(temperature), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]),
                             _stream(stream)), "ripe_accept")
     return tuple(out)
+
+
+def _on_device(t: torch.Tensor):
+    """The device of `t`, made current if it is not (the C entry points launch on the current device)."""
+    return torch.cuda.device(t.device)
+
+
+def _pages(K: torch.Tensor, V: torch.Tensor) -> ripe_pages_t:
+    npages, Hkv, page, d = K.shape
+    assert V.shape == K.shape and V.dtype == K.dtype and V.device == K.device
+    ps, hs, js, one = K.stride()
+    assert one == 1 and V.stride() == (ps, hs, js, 1), "the channels of a page's rows are adjacent; K and V lie alike"
+    return ripe_pages_t(K.data_ptr(), V.data_ptr(), ps, hs, js, npages, page, Hkv, d, _dtype_code(K.dtype))
+
+
+def _batch(table, ctx_len, row0, nrows, max_ntok, err, device) -> ripe_paged_batch_t:
+    nseq = ctx_len.numel()
+    for t in (table, ctx_len, row0) + (() if err is None else (err,)):
+        assert t.dtype == torch.int32 and t.device == device
+    assert table.dim() == 2 and table.shape[0] == nseq and row0.numel() == nseq + 1
+    assert ctx_len.is_contiguous() and row0.is_contiguous() and (table.shape[1] == 1 or table.stride(1) == 1)
+    return ripe_paged_batch_t(table.data_ptr(), table.stride(0), ctx_len.data_ptr(), row0.data_ptr(), table.shape[1], nseq,
+                              nrows, max_ntok, None if err is None else err.data_ptr())
+
+
+def _rows(t: torch.Tensor, pages: torch.Tensor, heads: int) -> int:
+    """Checks a row array [nrows][heads][d] beside its pages; the elements between two rows."""
+    assert t.dim() == 3 and t.dtype == pages.dtype and t.device == pages.device
+    assert t.shape[1] == heads and t.shape[2] == pages.shape[3]
+    assert t.stride(2) == 1 and (heads == 1 or t.stride(1) == t.shape[2]), "a row's heads are adjacent"
+    return t.stride(0) if t.shape[0] > 1 else heads * t.shape[2]
+
+
+def ripe_paged_append(K: torch.Tensor, V: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor, table: torch.Tensor,
+                      ctx_len: torch.Tensor, row0: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None):
+    """Write the new tokens' K and V ([nrows][Hkv][d], rows of any one stride) into the
+    pages ([npages][Hkv][page][d], any strides): sequence i's rows row0[i]..row0[i+1]-1
+    go behind its ctx_len[i] positions, through row i of the page table (int32
+    [nseq][width]).  err: device int32, see ripe.h."""
+    assert K.shape == V.shape
+    stride = _rows(K, Kpages, Kpages.shape[1])
+    assert _rows(V, Vpages, Vpages.shape[1]) == stride, "K and V have one row stride"
+    pages = _pages(Kpages, Vpages)
+    batch = _batch(table, ctx_len, row0, K.shape[0], max(1, K.shape[0]), err, K.device)
+    with _on_device(K):
+        _check(_lib.ripe_paged_append(ctypes.byref(pages), ctypes.byref(batch), K.data_ptr(), V.data_ptr(), stride,
+                                      _stream(stream)), "ripe_paged_append")
+
+
+def ripe_paged_attn_workspace(Kpages: torch.Tensor, H: int, max_ntok: int) -> int:
+    """Bytes of device work space a ripe_paged_attn call needs."""
+    pages = _pages(Kpages, Kpages)
+    out = ctypes.c_size_t()
+    with _on_device(Kpages):
+        _check(_lib.ripe_paged_attn_workspace(ctypes.byref(pages), H, max_ntok, ctypes.byref(out)),
+               "ripe_paged_attn_workspace")
+    return out.value
+
+
+def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor, table: torch.Tensor, ctx_len: torch.Tensor,
+                    row0: torch.Tensor, O: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                    max_ntok: Optional[int] = None, window: int = 0, sinks: int = 0, scale: float = 0.0,
+                    work: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None):
+    """Attention of the batch's new tokens over the pages that hold them already.  Q, O:
+    [nrows][H][d]; lse: float32 [nrows][H]; the batch as for ripe_paged_append.
+    max_ntok: host bound on one sequence's new tokens (None: nrows; a decode batch gives
+    1).  work: device bytes (None: taken from torch's allocator for this call)."""
+    nrows, H, d = Q.shape
+    if max_ntok is None:
+        max_ntok = max(1, nrows)
+    qs = _rows(Q, Kpages, H)
+    os_ = _rows(O, Kpages, H)
+    assert O.shape == Q.shape
+    assert lse is None or (lse.dtype == torch.float32 and lse.shape == (nrows, H) and lse.is_contiguous()
+                           and lse.device == Q.device)
+    pages = _pages(Kpages, Vpages)
+    batch = _batch(table, ctx_len, row0, nrows, max_ntok, err, Q.device)
+    with _on_device(Q):
+        if work is None:
+            need = ctypes.c_size_t()
+            _check(_lib.ripe_paged_attn_workspace(ctypes.byref(pages), H, max_ntok, ctypes.byref(need)),
+                   "ripe_paged_attn_workspace")
+            work = torch.empty(need.value, dtype=torch.uint8, device=Q.device)
+            if stream is not None:
+                work.record_stream(stream)
+        assert work.device == Q.device and work.is_contiguous()
+        _check(_lib.ripe_paged_attn(ctypes.byref(pages), ctypes.byref(batch), H, Q.data_ptr(), qs, window, sinks, scale,
+                                    O.data_ptr(), os_, None if lse is None else lse.data_ptr(), work.data_ptr(),
+                                    work.numel() * work.element_size(), _stream(stream)), "ripe_paged_attn")
 
 
 def ripe_cache_bytes(layers, R, H, d, W, Tmax, max_seqs, kmax, dtype=torch.bfloat16) -> int:

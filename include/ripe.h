@@ -71,8 +71,11 @@ enum {
     RIPE_DEVERR_BRANCH = 5,      /* a branch with depth outside [1,R], rows out of range, more tokens
                                     than the cache's kmax, or a sequence's branches not adjacent */
     RIPE_DEVERR_TIMEOUT = 6,     /* a kernel's bounded wait expired; its outputs are incomplete */
-    RIPE_DEVERR_FORK = 7         /* a fork pair with an id out of range, parent == child, or a parent
+    RIPE_DEVERR_FORK = 7,        /* a fork pair with an id out of range, parent == child, or a parent
                                     that is itself a fork; that pair was skipped */
+    RIPE_DEVERR_ROWS = 8,        /* a sequence's row offsets descend, leave [0, nrows] or hold more than
+                                    max_ntok tokens; that sequence was skipped */
+    RIPE_DEVERR_PAGE = 9         /* a page id outside [0, npages): read as page 0, not written */
 };
 
 /*
@@ -363,6 +366,87 @@ int ripe_cache_set_all_depths_kernel(ripe_cache_t cache, int kernel);
 int ripe_accept(int nseq, int k, int V, const float* zp, const float* zq, const float* zf, const int32_t* x1,
                 const int32_t* x2, const float* u, float temperature, int32_t* n_accepted, int32_t* token,
                 int32_t* path, ripe_stream_t stream);
+
+/*
+ * Pages of a single-plane key/value cache.  A looped model's prelude and coda layers
+ * run once per token, so they keep one plane per position (the closed-form memory
+ * fraction counts them so); their cache is a pool of pages of `page` positions each,
+ * and a table per sequence says which page holds positions i*page .. i*page+page-1.
+ *   K, V: device, element (p, h, j, c) of page p, key/value head h, slot j, channel c
+ *         at p*page_stride + h*head_stride + j*pos_stride + c (elements; the same for
+ *         both), so head-major and token-major pools are both read as they lie.  A
+ *         stride is at least d and a multiple of 16 bytes; that of a dimension of
+ *         size 1 is not used.
+ *   page: a power of two in [16, 1024].  1 <= Hkv <= 256; d as for ripe_cache_create.
+ * The caller owns the pool and the tables, and allocates pages.  Different sequences
+ * may share pages that are only read (a common prefix).
+ */
+typedef struct {
+    void* K;
+    void* V;
+    int64_t page_stride, head_stride, pos_stride;
+    int32_t npages, page, Hkv, d, dtype;
+    int32_t reserved[3]; /* must be 0 */
+} ripe_pages_t;
+
+/*
+ * A batch of new tokens over pages, as the two calls below take it: sequence i of nseq
+ * (0 <= nseq <= 1024) has ctx_len[i] cached positions and its new tokens are rows
+ * row0[i] .. row0[i+1]-1 of the row arrays (none is allowed), at positions ctx_len[i],
+ * ctx_len[i]+1, ...  table: int32 [nseq][table_width], row i at table + i*table_stride;
+ * entries past a sequence's last page are not read.  All of it is read on the device,
+ * so a call captured into a CUDA graph replays with new lengths and pages.  A sequence
+ * whose offsets are wrong (RIPE_DEVERR_ROWS) or whose tokens do not fit its
+ * table_width*page <= 2^30 positions (RIPE_DEVERR_CAPACITY) is skipped: its rows are
+ * left as they were, and so are rows that belong to no sequence.  err_dev (device int32,
+ * or NULL) receives the first such condition, like a cache's device error word.
+ */
+typedef struct {
+    const int32_t* table;
+    int64_t table_stride;
+    const int32_t* ctx_len;
+    const int32_t* row0; /* nseq + 1 */
+    int32_t table_width, nseq, nrows;
+    int32_t max_ntok; /* host bound on one sequence's new tokens, >= 1; nrows is always one */
+    int32_t* err_dev;
+} ripe_paged_batch_t;
+
+/*
+ * Write the batch's new keys and values into the pages: row r of K and V
+ * ([nrows][Hkv][d] in the pool's dtype, rows row_stride >= Hkv*d elements apart, a
+ * multiple of 16 bytes) goes to its token's position.  Tokens whose page id is out of
+ * range are not written (RIPE_DEVERR_PAGE).  max_ntok is not used.
+ */
+int ripe_paged_append(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, const void* K, const void* V,
+                      int64_t row_stride, ripe_stream_t stream);
+
+/*
+ * Attention of the batch's new tokens over the pages, which hold their keys and values
+ * already (ripe_paged_append): the token at position t sees positions p <= t with
+ * window == 0, or p > t - window, or p < sinks (the first tokens, which stay visible
+ * behind a sliding window).  s = scale*<q,k>, O = softmax(s) V, accumulated in fp32;
+ * bf16 weights in the second product (P is rounded once, 2^-8 relative at most).  Query head h
+ * reads key/value head h / (H/Hkv).  One token per sequence is a decode step, a few
+ * are a draft block under verification, thousands a prompt or a chunk of one; a batch
+ * may mix them.
+ *   Q, O: device, [nrows][H][d] in the pool's dtype, rows q_stride and o_stride >= H*d
+ *         elements apart, multiples of 16 bytes.  lse: float [nrows][H] or NULL.
+ *   H: a multiple of Hkv, at most 256; H/Hkv at most 128 (bf16 with d in {64, 96,
+ *         128}) or 16 (otherwise), RIPE_ERR_UNSUPPORTED beyond.
+ *   scale: > 0 and finite; 0 means 1/sqrt(d).  window, sinks >= 0.
+ *   work: device, 256-byte aligned, work_bytes >= what ripe_paged_attn_workspace says
+ *         for these sizes (RIPE_ERR_CAPACITY otherwise); need not be initialised.  Calls
+ *         that may overlap on the GPU, replays of captured ones included, need one each.
+ * What lies in slots past a sequence's last token, and in keys a token does not see, has
+ * no influence, whatever it is (infinities and NaN included).  A page id out of range is
+ * read as page 0 (RIPE_DEVERR_PAGE): that sequence's rows then mean nothing.
+ * max_ntok*(H/Hkv) <= 16 takes a kernel made for few rows per key; with bf16 and d in
+ * {64, 96, 128} more rows run on tcgen05; all else runs on CUDA cores.
+ */
+int ripe_paged_attn_workspace(const ripe_pages_t* pages, int H, int max_ntok, size_t* bytes);
+int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, int H, const void* Q, int64_t q_stride,
+                    int window, int sinks, float scale, void* O, int64_t o_stride, float* lse, void* work,
+                    size_t work_bytes, ripe_stream_t stream);
 
 /*
  * Test hook for the bounded-wait error path (the pages have no counterpart).  The

@@ -437,6 +437,25 @@ int ripe_accept(int nseq, int k, int V, const float* zp, const float* zq, const 
     return e == cudaSuccess ? RIPE_OK : cuda_fail(e, "accept launch");
 }
 
+int ripe_sample(int nrows, int V, const void* logits, int dtype, int64_t row_stride, const float* u,
+                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token,
+                float* logprob, ripe_stream_t stream) {
+    if (nrows < 0 || nrows > (1 << 20)) return fail(RIPE_ERR_INVALID_ARG, "nrows=%d outside [0, 2^20]", nrows);
+    if (V < 1 || V > (1 << 23)) return fail(RIPE_ERR_INVALID_ARG, "V=%d outside [1, 2^23]", V);
+    if (dtype != RIPE_BF16 && dtype != RIPE_F32) return fail(RIPE_ERR_INVALID_ARG, "dtype=%d", dtype);
+    if (nrows > 1 && row_stride < V)
+        return fail(RIPE_ERR_INVALID_ARG, "row_stride=%lld < V=%d", (long long)row_stride, V);
+    if (nrows == 0) return RIPE_OK;
+    if (!logits || !u || !token) return fail(RIPE_ERR_INVALID_ARG, "NULL pointer argument");
+    const auto mis = [](const void* p) { return ((uintptr_t)p & 3u) != 0; };
+    if (((uintptr_t)logits & (dtype == RIPE_BF16 ? 1u : 3u)) || mis(u) || mis(temperature) || mis(top_k) || mis(top_p) ||
+        mis(min_p) || mis(token) || mis(logprob))
+        return fail(RIPE_ERR_UNALIGNED, "arrays must be aligned to their elements");
+    cudaError_t e = launch_sample(nrows, V, logits, dtype == RIPE_BF16, row_stride, u, temperature, top_k, top_p, min_p,
+                                  token, logprob, as_stream(stream));
+    return e == cudaSuccess ? RIPE_OK : cuda_fail(e, "sample launch");
+}
+
 int ripe_debug_stall_next_verify(ripe_cache_t c, long long cycles) {
     int rc = check_cache(c);
     if (rc != RIPE_OK) return rc;

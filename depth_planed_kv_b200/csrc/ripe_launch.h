@@ -70,6 +70,10 @@ cudaError_t launch_accept(int nseq, int k, int V, const float* zp, const float* 
                           const int32_t* x2, const float* u, float temperature, int32_t* n_acc, int32_t* token,
                           int32_t* path, cudaStream_t st);
 
+cudaError_t launch_sample(int nrows, int V, const void* z, int bf16, int64_t row_stride, const float* u,
+                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                          int32_t* token, float* logprob, cudaStream_t st);
+
 // `part`: scratch for the partial results (plan.part_bytes).
 cudaError_t launch_verify(const ripe_cache_s* c, const VerifyPlan& plan, int layer, const BranchArgs& ba,
                           const void* Q, const void* Kb, const void* Vb, const int32_t* ctx, float scale,

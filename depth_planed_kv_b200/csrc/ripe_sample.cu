@@ -1,0 +1,600 @@
+// ripe_sample.cu -- the draw of one token per row of logits, with temperature, top-k,
+// top-p and min-p, from given uniforms.
+//
+// With m = max_v z_v and w_v = exp((z_v - m) / T), and the tokens in the order (z
+// descending, v ascending), the kept set is a prefix of that order:
+//   top-k   the first k tokens;
+//   top-p   those with (mass before them) < p * (mass of the first k), at least one;
+//   min-p   those with w_v >= min_p (w of the first token is 1).
+// The token is the smallest v whose running sum of kept w, in index order, exceeds u
+// times the kept mass; its log probability is log(w_v / kept mass).
+//
+// A draw is a comparison of running sums with a border, so the sums must not depend on
+// rounding or on the order of additions: weights are computed in 64 bits and held as
+// integers of 2^-40 (a sum of 2^23 weights stays below 2^64), which add up exactly in
+// any order.  A row of V near-equal tokens has V borders 1/V apart; an error of 2^-41 of
+// the largest weight moves a border by at most 2^-41, where 32-bit sums would pick
+// another token in about one of 10^4 rows.
+//
+// One cluster of 1 to 8 CTAs per row; each CTA holds a contiguous slice of the row in
+// shared memory, so the logits are read from memory once.  The k-th token, and the one
+// where the mass passes p, are found by counting and summing into 1024 bins (linear in
+// z first, then linear in the ordered bit pattern inside the bin that holds the border)
+// until the bin holds one token or one value; CTAs exchange their bins through
+// distributed shared memory, one cluster barrier per level.
+#include <math.h>
+
+#include "ripe_internal.cuh"
+#include "ripe_launch.h"
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 1024;
+constexpr int kMaxCluster = 8;
+constexpr double kOne = 1099511627776.0;  // 2^40: weight 1
+constexpr float kRange = 28.f;            // w < 2^-40 beyond this many units of T below the maximum
+
+typedef unsigned long long u64;
+
+struct SampleArgs {
+    const void* z;
+    int64_t row_stride;
+    int nrows, V, per, seg;  // per: tokens of one CTA; seg: tokens of one warp (a multiple of 32)
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t* top_k;
+    int32_t* token;
+    float* logprob;
+};
+
+// What a CTA tells the others of its cluster; two of them in turn, so that one cluster
+// barrier per exchange is enough.
+struct Msg {
+    u64 sum;
+    float mx;
+    int idx;
+};
+
+struct Shared {
+    unsigned cnt[2][kBins], lo[2][kBins], hi[2][kBins];  // bins: tokens, mass (low and high words)
+    Msg msg[2][kMaxCluster];
+    u64 wsum[kWarps];
+    float wmax[kWarps];
+    int widx[kWarps];
+    u64 scan[kWarps];
+    u64 pick[5];
+};
+
+__device__ __forceinline__ unsigned cluster_size() {
+    unsigned n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned n;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+    return n;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+// The address of `p` (shared memory of this CTA) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer(const void* p, unsigned rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ unsigned peer_ld(uint32_t a) {
+    unsigned x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ void peer_st(uint32_t a, unsigned x) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+
+__device__ __forceinline__ float to_logit(float x) { return x != x ? -INFINITY : x + 0.f; }  // NaN: never drawn; -0 = 0
+__device__ __forceinline__ float load_logit(const float* z, int64_t i) { return to_logit(__ldg(z + i)); }
+__device__ __forceinline__ float load_logit(const __nv_bfloat16* z, int64_t i) { return to_logit(__bfloat162float(z[i])); }
+
+// The bit pattern of a logit as an integer of the same order.
+__device__ __forceinline__ unsigned key_of(float x) {
+    const unsigned b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+struct Row {
+    float m, scale0;  // maximum; bins per unit of z at the first level
+    double dm, it;    // maximum, 1 / T
+    // weight of logit x in units of 2^-40
+    __device__ __forceinline__ u64 weight(float x) const {
+        if (x == m) return (u64)kOne;
+        const double y = ((double)x - dm) * it;
+        return y > -30.0 ? (u64)__double2ull_rn(exp(y) * kOne) : 0ull;
+    }
+    // first-level bin: linear in z, largest first; monotone
+    __device__ __forceinline__ int bin0(float x) const {
+        return x == m ? 0 : (int)fminf((m - x) * scale0, (float)(kBins - 1));
+    }
+};
+
+template <typename Elem, bool RES>
+struct Cta {
+    const SampleArgs& a;
+    Shared& sh;
+    float* sx;
+    const Elem* z;
+    int n;  // tokens of this CTA's slice
+    unsigned rank, size;
+    int tid, warp, lane, phase = 0;  // phase: which Msg buffer is next
+
+    __device__ __forceinline__ float get(int i) const { return RES ? sx[i] : load_logit(z, i); }
+
+    // f(i, x) for every token of the slice, each warp its contiguous segment in order.
+    template <typename F>
+    __device__ __forceinline__ void each(F&& f) const {
+        const int e = min(n, (warp + 1) * a.seg);
+#pragma unroll 4
+        for (int i = warp * a.seg + lane; i < e; i += 32) f(i, get(i));
+    }
+
+    // Tells every CTA of the cluster this CTA's (sum, mx, idx), and returns all of them.
+    __device__ __forceinline__ const Msg* exchange(u64 sum, float mx, int idx) {
+        Msg* buf = sh.msg[phase];
+        phase ^= 1;
+        if (tid < (int)size) {
+            const uint32_t d = peer(buf + rank, tid);
+            peer_st(d, (unsigned)sum);
+            peer_st(d + 4, (unsigned)(sum >> 32));
+            peer_st(d + 8, __float_as_uint(mx));
+            peer_st(d + 12, (unsigned)idx);
+        }
+        cluster_sync();
+        return buf;
+    }
+
+    __device__ __forceinline__ u64 block_sum(u64 v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        __syncthreads();
+        if (lane == 0) sh.wsum[warp] = v;
+        __syncthreads();
+        u64 t = 0;
+        for (int w = 0; w < kWarps; ++w) t += sh.wsum[w];
+        return t;
+    }
+
+    // Bins of one level, of all CTAs: finds the bin where the running count (mass == false)
+    // or mass passes `target`: the first bin with before < target <= before + own.  Returns
+    // the bin; before_cnt, before_mass grow by what lies in the bins ahead of it; own: its
+    // count and mass.
+    __device__ int find_bin(int b, bool mass, double target, u64& before_cnt, u64& before_mass, u64& own_cnt,
+                            u64& own_mass) {
+        constexpr int kPer = kBins / kThreads;
+        u64 c[kPer], s[kPer], ct = 0, st = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            c[j] = s[j] = 0;
+            const int i = tid * kPer + j;
+            for (unsigned r = 0; r < size; ++r) {
+                c[j] += peer_ld(peer(&sh.cnt[b][i], r));
+                s[j] += peer_ld(peer(&sh.lo[b][i], r)) + ((u64)peer_ld(peer(&sh.hi[b][i], r)) << 32);
+            }
+            ct += c[j];
+            st += s[j];
+        }
+        // exclusive prefix over the threads
+        u64 ci = ct, si = st;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 x = __shfl_up_sync(0xffffffffu, ci, o), y = __shfl_up_sync(0xffffffffu, si, o);
+            if (lane >= o) {
+                ci += x;
+                si += y;
+            }
+        }
+        __syncthreads();
+        if (lane == 31) {
+            sh.wsum[warp] = ci;
+            sh.scan[warp] = si;
+        }
+        if (tid == 0) sh.pick[0] = kBins;
+        __syncthreads();
+        u64 cb = before_cnt + ci - ct, sb = before_mass + si - st;
+        for (int w = 0; w < warp; ++w) {
+            cb += sh.wsum[w];
+            sb += sh.scan[w];
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const double lo = mass ? (double)sb : (double)cb, up = mass ? (double)(sb + s[j]) : (double)(cb + c[j]);
+            if (lo < target && target <= up) {
+                sh.pick[0] = tid * kPer + j;
+                sh.pick[1] = cb;
+                sh.pick[2] = sb;
+                sh.pick[3] = c[j];
+                sh.pick[4] = s[j];
+            }
+            cb += c[j];
+            sb += s[j];
+        }
+        __syncthreads();
+        const int bin = (int)sh.pick[0];
+        if (bin < kBins) {
+            before_cnt = sh.pick[1];
+            before_mass = sh.pick[2];
+            own_cnt = sh.pick[3];
+            own_mass = sh.pick[4];
+        }
+        __syncthreads();
+        return bin;
+    }
+
+    __device__ __forceinline__ void clear_bins(int b) {
+        for (int i = tid; i < kBins; i += kThreads) sh.cnt[b][i] = sh.lo[b][i] = sh.hi[b][i] = 0u;
+    }
+    __device__ __forceinline__ void add_bin(int b, int i, u64 w) {
+        atomicAdd(&sh.cnt[b][i], 1u);
+        if (w) {
+            const unsigned l = (unsigned)w, old = atomicAdd(&sh.lo[b][i], l);
+            const unsigned h = (unsigned)(w >> 32) + (old + l < old ? 1u : 0u);
+            if (h) atomicAdd(&sh.hi[b][i], h);
+        }
+    }
+};
+
+// The border of a prefix of the order: tokens with key > kt are in, and the first `c` (in
+// index order) of those with key == kt.
+struct Border {
+    unsigned kt;
+    u64 c;      // 0: none
+    u64 equal;  // tokens with key == kt (known when c > 0)
+    u64 mass;   // of the prefix
+};
+
+// From the first level's bins (buffer 0, complete) to the border; later levels use buffer 1.
+template <typename Elem, bool RES>
+__device__ Border find_border(Cta<Elem, RES>& t, const Row& row, bool mass, double target, bool with_mass) {
+    u64 bc = 0, bm = 0, oc = 0, om = 0;
+    const int b0 = t.find_bin(0, mass, target, bc, bm, oc, om);
+    Border r;
+    r.kt = 0;
+    r.c = 0;
+    r.equal = 0;
+    r.mass = bm + om;
+    // the keys that can lie in the bin (its edges, widened by the rounding of bin0)
+    const double w = 1.0 / (double)row.scale0, e = 1e-5 * (b0 + 1) * w + 1e-6 * fabs(row.dm);
+    unsigned khi = b0 == 0 ? key_of(row.m) : min(key_of(row.m), key_of((float)(row.dm - b0 * w + e)));
+    unsigned klo = b0 == kBins - 1 ? key_of(-INFINITY) : key_of((float)(row.dm - (b0 + 1) * w - e));
+    if (isinf(row.m)) {
+        khi = key_of(row.m);
+        klo = key_of(-INFINITY);
+    }
+    if (klo > khi) klo = khi;
+    auto inside = [&](float x, unsigned k) { return k >= klo && k <= khi && row.bin0(x) == b0; };
+    while (true) {
+        const bool all = mass ? oc == 1 : (double)(bc + oc) == target;
+        if (all) {  // the whole bin is in: the border lies below its last token
+            r.mass = bm + om;
+            r.kt = klo - 1;
+            r.c = 0;
+            // tokens of a neighbouring first-level bin may share the widened range; the bin's own
+            // smallest key is the border
+            unsigned least = 0xffffffffu;
+            t.each([&](int, float x) {
+                const unsigned k = key_of(x);
+                if (inside(x, k)) least = min(least, k);
+            });
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+            __syncthreads();
+            if (t.lane == 0) t.sh.widx[t.warp] = (int)least;
+            __syncthreads();
+            for (int i = 0; i < kWarps; ++i) least = min(least, (unsigned)t.sh.widx[i]);
+            const Msg* g = t.exchange(0, 0.f, (int)least);
+            for (unsigned i = 0; i < t.size; ++i) least = min(least, (unsigned)g[i].idx);
+            r.kt = least - 1;
+            return r;
+        }
+        if (klo == khi) {
+            r.kt = klo;
+            r.equal = oc;
+            const u64 w1 = oc ? om / oc : 0;
+            double c = mass ? ceil((target - (double)bm) / (double)(w1 ? w1 : 1)) : target - (double)bc;
+            r.c = (u64)fmin(fmax(c, 1.0), (double)oc);
+            r.mass = bm + r.c * w1;
+            return r;
+        }
+        // bins of the ordered bit pattern over [klo, khi], largest first
+        int shift = 0;
+        while (((khi - klo) >> shift) >= kBins) ++shift;
+        const int b = 1;
+        cluster_sync();  // nobody reads the bins of the level before any more
+        t.clear_bins(b);
+        __syncthreads();
+        t.each([&](int, float x) {
+            const unsigned k = key_of(x);
+            if (inside(x, k)) t.add_bin(b, (int)((khi - k) >> shift), with_mass ? row.weight(x) : 0ull);
+        });
+        cluster_sync();
+        const int i = t.find_bin(b, mass, target, bc, bm, oc, om);
+        const unsigned top = khi - ((unsigned)i << shift);
+        const unsigned span = (1u << shift) - 1;
+        if (i >= kBins) {  // cannot be: the bins hold what the bin before held
+            r.kt = klo - 1;
+            return r;
+        }
+        klo = top - klo > span ? top - span : klo;
+        khi = top;
+    }
+}
+
+template <typename Elem, bool RES>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem);
+    const unsigned size = cluster_size();
+    const int r = blockIdx.x / size;
+    Cta<Elem, RES> t{a, sh, reinterpret_cast<float*>(smem + sizeof(Shared)), nullptr, 0, cluster_rank(), size,
+                     (int)threadIdx.x, (int)threadIdx.x / 32, (int)threadIdx.x % 32};
+    cluster_arrive();  // waited for before the first word to another CTA: by then all have started
+    const int v0 = t.rank * a.per;
+    t.z = reinterpret_cast<const Elem*>(a.z) + r * a.row_stride + v0;
+    t.n = max(0, min(a.per, a.V - v0));
+
+    const float T = a.temperature ? __ldg(a.temperature + r) : 1.f;
+    const int k = a.top_k ? __ldg(a.top_k + r) : 0;
+    const float p = a.top_p ? __ldg(a.top_p + r) : 1.f;
+    const float mp = a.min_p ? __ldg(a.min_p + r) : 0.f;
+
+    // ---- the slice, and the largest logit (lowest index on ties)
+    float mx = -INFINITY;
+    int mi = 0x7fffffff;
+    {
+        const int e = min(t.n, (t.warp + 1) * a.seg);
+#pragma unroll 8
+        for (int i = t.warp * a.seg + t.lane; i < e; i += 32) {
+            const float x = load_logit(t.z, i);
+            if (RES) t.sx[i] = x;
+            if (x > mx) {
+                mx = x;
+                mi = i;
+            }
+        }
+    }
+    mi = mi == 0x7fffffff ? mi : mi + v0;
+    auto better = [&](float x, int i) {
+        if (x > mx || (x == mx && i < mi)) {
+            mx = x;
+            mi = i;
+        }
+    };
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float x = __shfl_xor_sync(0xffffffffu, mx, o);
+        const int i = __shfl_xor_sync(0xffffffffu, mi, o);
+        better(x, i);
+    }
+    if (t.lane == 0) {
+        sh.wmax[t.warp] = mx;
+        sh.widx[t.warp] = mi;
+    }
+    t.clear_bins(0);
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) better(sh.wmax[w], sh.widx[w]);
+    cluster_wait();
+    {
+        const Msg* g = t.exchange(0, mx, mi);
+        for (unsigned i = 0; i < size; ++i) better(g[i].mx, g[i].idx);
+    }
+    const bool writer = t.rank == 0 && t.tid == 0;
+    // Every CTA of the cluster takes the same way out; the last barrier keeps shared memory
+    // alive for the others' reads.
+    if (mx == -INFINITY || !(T > 0.f) || k == 1 || mp > 1.f || p <= 0.f) {
+        if (writer) {
+            a.token[r] = mx == -INFINITY ? -1 : mi;
+            if (a.logprob) a.logprob[r] = mx == -INFINITY ? -INFINITY : 0.f;
+        }
+        cluster_sync();
+        return;
+    }
+    Row row;
+    row.m = mx;
+    row.dm = mx;
+    row.it = 1.0 / (double)T;
+    row.scale0 = fminf(fmaxf((float)kBins / (kRange * T), 1e-30f), 1e30f);
+
+    // ---- the border of top-k and top-p
+    const bool need_k = k > 0 && k < a.V, need_p = p < 1.f;
+    Border bd;
+    bd.kt = 0;
+    bd.c = 0;
+    bd.equal = 0;
+    if (need_k || need_p) {
+        unsigned last = 0;  // tokens of the last bin, most of them: counted apart
+        t.each([&](int, float x) {
+            const int b = row.bin0(x);
+            const u64 w = need_p ? row.weight(x) : 0ull;
+            if (b == kBins - 1 && w == 0) ++last;
+            else t.add_bin(0, b, w);
+        });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(0xffffffffu, last, o);
+        if (t.lane == 0 && last) atomicAdd(&sh.cnt[0][kBins - 1], last);
+        u64 total = 0;
+        if (need_p) {
+            __syncthreads();
+            u64 s = 0;
+            for (int i = t.tid; i < kBins; i += kThreads) s += sh.lo[0][i] + ((u64)sh.hi[0][i] << 32);
+            s = t.block_sum(s);
+            const Msg* g = t.exchange(s, 0.f, 0);
+            for (unsigned i = 0; i < size; ++i) total += g[i].sum;
+        } else {
+            cluster_sync();
+        }
+        if (need_k) {
+            bd = find_border(t, row, false, (double)k, need_p);
+            total = bd.mass;
+        }
+        if (need_p) bd = find_border(t, row, true, (double)p * (double)total, true);
+    }
+    // ---- of the tokens at the border, the first c in index order: the last one's index
+    int last_equal = 0x7fffffff;
+    if (bd.c > 0 && bd.c < bd.equal) {
+        u64 n = 0;
+        t.each([&](int, float x) { n += key_of(x) == bd.kt; });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        const u64 mine = n;
+        const u64 all = t.block_sum(t.lane == 0 ? n : 0ull);
+        const Msg* g = t.exchange(all, 0.f, 0);
+        u64 before = 0;
+        for (unsigned i = 0; i < t.rank; ++i) before += g[i].sum;
+        for (int w = 0; w < t.warp; ++w) before += sh.wsum[w];
+        int found = 0x7fffffff;
+        if (before < bd.c && bd.c <= before + mine) {
+            const int e = min(t.n, (t.warp + 1) * a.seg);
+            for (int i0 = t.warp * a.seg; i0 < e; i0 += 32) {
+                const int i = i0 + t.lane;
+                const unsigned hit = __ballot_sync(0xffffffffu, i < e && key_of(t.get(i)) == bd.kt);
+                const u64 want = bd.c - before;  // >= 1
+                if (want <= (u64)__popc(hit)) {
+                    unsigned rest = hit;
+                    for (u64 j = 1; j < want; ++j) rest &= rest - 1;
+                    found = v0 + i0 + __ffs(rest) - 1;
+                    break;
+                }
+                before += __popc(hit);
+            }
+        }
+        __syncthreads();
+        if (t.lane == 0) sh.widx[t.warp] = found;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) found = min(found, sh.widx[w]);
+        const Msg* h = t.exchange(0, 0.f, found);
+        for (unsigned i = 0; i < size; ++i) last_equal = min(last_equal, h[i].idx);
+    }
+    const double low = mp > 0.f ? log((double)mp) * (double)T : -INFINITY;
+    auto kept = [&](int i, float x) {
+        const unsigned q = key_of(x);
+        const bool in = q > bd.kt || (bd.c > 0 && q == bd.kt && v0 + i <= last_equal) || !(need_k || need_p);
+        return in && (x == row.m || (double)x - row.dm >= low);
+    };
+    // ---- the draw
+    u64 s = 0;
+    t.each([&](int i, float x) {
+        if (kept(i, x)) s += row.weight(x);
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const u64 mine = s;
+    const u64 cta = t.block_sum(t.lane == 0 ? s : 0ull);
+    const Msg* g = t.exchange(cta, 0.f, 0);
+    u64 before = 0, W = 0;
+    for (unsigned i = 0; i < size; ++i) {
+        if (i < t.rank) before += g[i].sum;
+        W += g[i].sum;
+    }
+    for (int w = 0; w < t.warp; ++w) before += sh.wsum[w];
+    const float u = __ldg(a.u + r);
+    // u outside [0, 1) is taken as its nearer end (at 1: the last token with weight)
+    const double goal = fmin(u > 0.f ? (double)u : 0.0, 1.0 - 0x1p-50) * (double)W;
+    auto emit = [&](int i) {
+        a.token[r] = v0 + i;
+        const double y = ((double)t.get(i) - row.dm) * row.it;
+        if (a.logprob) a.logprob[r] = (float)((t.get(i) == row.m ? 0.0 : y) - log((double)W / kOne));
+    };
+    if (goal < 1.0) {
+        // u below the resolution: the first kept token of any weight at all
+        int first = 0x7fffffff;
+        t.each([&](int i, float x) {
+            if (kept(i, x) && (x == row.m || ((double)x - row.dm) * row.it > -745.0)) first = min(first, i);
+        });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+        __syncthreads();
+        if (t.lane == 0) sh.widx[t.warp] = first;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) first = min(first, sh.widx[w]);
+        const Msg* h = t.exchange(0, 0.f, first);
+        int owner = -1;
+        for (int i = (int)size - 1; i >= 0; --i)
+            if (h[i].idx != 0x7fffffff) owner = i;
+        if (owner == (int)t.rank && t.tid == 0) emit(first);
+    } else if ((double)before <= goal && (double)(before + mine) > goal) {
+        const int e = min(t.n, (t.warp + 1) * a.seg);
+        for (int i0 = t.warp * a.seg; i0 < e; i0 += 32) {
+            const int i = i0 + t.lane;
+            u64 w = 0;
+            if (i < e) {
+                const float x = t.get(i);
+                if (kept(i, x)) w = row.weight(x);
+            }
+            u64 inc = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (t.lane >= o) inc += y;
+            }
+            const unsigned over = __ballot_sync(0xffffffffu, (double)(before + inc) > goal);
+            if (over) {
+                if (t.lane == __ffs(over) - 1) emit(i);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
+        }
+    }
+    cluster_sync();
+}
+
+template <typename Elem, bool RES>
+cudaError_t launch_t(SampleArgs a, int cluster, cudaStream_t st) {
+    static PerDeviceOnce once;
+    constexpr int kMost = 232448;
+    cudaError_t e = per_device_once(once, [] {
+        return cudaFuncSetAttribute(sample_kernel<Elem, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.nrows * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared) + (RES ? (size_t)a.per * 4 : 0);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    ripe_count_launch();
+    return cudaLaunchKernelEx(&cfg, sample_kernel<Elem, RES>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(int nrows, int V, const void* z, int bf16, int64_t row_stride, const float* u,
+                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                          int32_t* token, float* logprob, cudaStream_t st) {
+    SampleArgs a;
+    a.z = z;
+    a.row_stride = row_stride;
+    a.nrows = nrows;
+    a.V = V;
+    a.u = u;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.token = token;
+    a.logprob = logprob;
+    int cluster = 1;
+    while (cluster < kMaxCluster && V > cluster * 2048) cluster *= 2;
+    a.per = (V + cluster - 1) / cluster;
+    a.seg = (a.per + 32 * kWarps - 1) / (32 * kWarps) * 32;
+    const bool res = sizeof(Shared) + (size_t)a.per * 4 <= 232448;
+    if (bf16) return res ? launch_t<__nv_bfloat16, true>(a, cluster, st) : launch_t<__nv_bfloat16, false>(a, cluster, st);
+    return res ? launch_t<float, true>(a, cluster, st) : launch_t<float, false>(a, cluster, st);
+}

@@ -89,6 +89,7 @@ _sig("ripe_cache_verify_path", [_P, ctypes.POINTER(_I)])
 _sig("ripe_cache_set_all_depths_kernel", [_P, _I])
 _sig("ripe_debug_stall_next_verify", [_P, ctypes.c_longlong])
 _sig("ripe_accept", [_I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P])
+_sig("ripe_sample", [_I, _I, _P, _I, ctypes.c_int64] + [_P] * 8)
 _sig("ripe_paged_append", [_P, _P, _P, _P, ctypes.c_int64, _P])
 _sig("ripe_paged_attn_workspace", [_P, _I, _I, ctypes.POINTER(ctypes.c_size_t)])
 _sig("ripe_paged_attn", [_P, _P, _I, _P, ctypes.c_int64, _I, _I, ctypes.c_float, _P, ctypes.c_int64, _P, _P,
@@ -104,7 +105,7 @@ EXPORTED = ["ripe_cache_bytes", "ripe_cache_create", "ripe_cache_destroy", "ripe
             "ripe_append", "ripe_evict", "ripe_truncate", "ripe_fork", "ripe_read_forks", "ripe_verify_attn",
             "ripe_verify_attn_all_depths", "ripe_verify_attn_all_depths_sliding", "ripe_verify_attn_noalloc", "ripe_reserve_workspace",
             "ripe_synth_fill", "ripe_cache_verify_path", "ripe_cache_set_all_depths_kernel",
-            "ripe_debug_stall_next_verify", "ripe_accept",
+            "ripe_debug_stall_next_verify", "ripe_accept", "ripe_sample",
             "ripe_paged_append", "ripe_paged_attn_workspace", "ripe_paged_attn",
             "ripe_cache_buffers", "ripe_read_meta", "ripe_get_device_error", "ripe_launch_count",
             "ripe_error_string", "ripe_last_error"]
@@ -164,6 +165,30 @@ def ripe_accept(zp: torch.Tensor, zq: torch.Tensor, zf: Optional[torch.Tensor], 
 def _on_device(t: torch.Tensor):
     """The device of `t`, made current if it is not (the C entry points launch on the current device)."""
     return torch.cuda.device(t.device)
+
+
+def ripe_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+                top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                min_p: Optional[torch.Tensor] = None, stream=None):
+    """One token per row of logits (float32 or bfloat16 [nrows][V], rows of any stride)
+    from the uniforms u (float32 [nrows]).  temperature, top_p, min_p (float32) and top_k
+    (int32): [nrows] each, or None.  Returns (token int32 [nrows], logprob float32
+    [nrows])."""
+    n, V = logits.shape
+    assert V == 1 or logits.stride(1) == 1, "a row's logits are adjacent"
+    for t, dt in ((u, torch.float32), (temperature, torch.float32), (top_k, torch.int32), (top_p, torch.float32),
+                  (min_p, torch.float32)):
+        assert t is None or (t.dtype == dt and t.shape == (n,) and t.is_contiguous() and t.device == logits.device)
+    with _on_device(logits):
+        token = torch.empty(n, dtype=torch.int32, device=logits.device)
+        logprob = torch.empty(n, dtype=torch.float32, device=logits.device)
+        if stream is not None:
+            token.record_stream(stream)
+            logprob.record_stream(stream)
+        _check(_lib.ripe_sample(n, V, _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), _ptr(u), _ptr(temperature),
+                                _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(logprob), _stream(stream)),
+               "ripe_sample")
+    return token, logprob
 
 
 def _pages(K: torch.Tensor, V: torch.Tensor) -> ripe_pages_t:

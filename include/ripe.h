@@ -368,6 +368,31 @@ int ripe_accept(int nseq, int k, int V, const float* zp, const float* zq, const 
                 int32_t* path, ripe_stream_t stream);
 
 /*
+ * The draw of one token per row of logits, from given uniforms: the draft tokens x1 and
+ * x2 that ripe_accept takes, or the next token of a plain decode step.
+ *   logits: device, [nrows] rows of V elements of dtype (RIPE_F32 or RIPE_BF16), rows
+ *       row_stride >= V elements apart, any element alignment.  1 <= V <= 2^23.
+ *   u: device float [nrows] in [0, 1).
+ *   temperature, top_k, top_p, min_p: device arrays [nrows], each row its own settings;
+ *       NULL, or a row's neutral value, switches one off: temperature 1, top_k <= 0 or
+ *       >= V, top_p >= 1, min_p <= 0.  temperature <= 0 is greedy (the largest logit).
+ * With m = max z and w_v = exp((z_v - m) / temperature), and the tokens ordered by z
+ * (largest first, lowest index first on ties), these are kept: the first top_k; of
+ * them, while the mass before a token is below top_p times the mass of the first top_k;
+ * of them, those with w_v >= min_p.  The first token is always kept.  The token drawn is
+ * the smallest v whose running sum of kept w, in index order, exceeds u times the kept
+ * mass (ripe_accept's draw).  A NaN logit counts as -inf; a row without any logit above
+ * -inf gives token -1.
+ * Outputs: token (device int32 [nrows]) and logprob (device float [nrows], or NULL): the
+ * natural logarithm of the token's share of the kept mass (0 when greedy).
+ * Weights are computed in 64 bits and summed exactly (in units of 2^-40 of the largest),
+ * so the same inputs give the same token whatever the launch.
+ */
+int ripe_sample(int nrows, int V, const void* logits, int dtype, int64_t row_stride, const float* u,
+                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token,
+                float* logprob, ripe_stream_t stream);
+
+/*
  * Pages of a single-plane key/value cache.  A looped model's prelude and coda layers
  * run once per token, so they keep one plane per position (the closed-form memory
  * fraction counts them so); their cache is a pool of pages of `page` positions each,

@@ -127,24 +127,35 @@ struct PagedSeg {
 
 struct PagedPlanSmem {
     int sq[kPagedMaxSeqs + 1];  // row tiles before each sequence
-    int64_t tp[512 + 1];        // cost before each thread's run of row tiles (one head)
-    int64_t warp[16];
+    int64_t warp[17];
+    PagedSeg s;                 // where the CTA's stretch begins, as one thread finds it
+    int qt, off;
 };
 
-// Inclusive block-wide scan of one value per thread (all threads call it).
-template <typename T>
-__device__ __forceinline__ T paged_scan(T v, T* warp_sums) {
+// Inclusive block-wide scan of one value per thread (all threads call it; one barrier).
+template <int THREADS, typename T>
+__device__ __forceinline__ T paged_scan(T v, T* warp_sums, T& total) {
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const T y = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += y;
     }
-    __syncthreads();
     if (lane == 31) warp_sums[w] = v;
     __syncthreads();
-    for (int i = 0; i < w; ++i) v += warp_sums[i];
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < w) v += warp_sums[i];
+        total += warp_sums[i];
+    }
     return v;
+}
+
+// a / b for a >= 0, b > 0: the 32-bit division where it fits (most calls), a fraction of
+// the other's cost.
+__device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
+    return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 template <int KT>
@@ -169,64 +180,104 @@ struct PagedPlan {
         s.r = q.r;
     }
 
+    // The CTA's stretch of the line, given that the one-head cost `p` lies before the
+    // current item (the item that holds x / Hkv).
+    __device__ __forceinline__ void place(const PagedArgs& a, int64_t p) {
+        const int c = item(a);
+        const int64_t rem = x - p * a.Hkv;
+        s.head = (int)paged_div(rem, c);
+        off = (int)(rem - (int64_t)s.head * c);
+    }
+    __device__ __forceinline__ void share(const PagedArgs& a, int64_t one_head, int min_cost) {
+        const int64_t total = one_head * a.Hkv;
+        int64_t len = paged_div(total + gridDim.x - 1, gridDim.x);
+        len = len < min_cost ? min_cost : len;
+        x = len * blockIdx.x;
+        x_end = x + len < total ? x + len : total;
+    }
+
     // All threads of the block; `sm` may be reused after the call (it ends with a barrier).
     template <int THREADS>
     __device__ void begin(const PagedArgs& a, PagedPlanSmem& sm, int min_cost) {
         static_assert(THREADS <= 512, "one run of row tiles per thread");
         const int tid = threadIdx.x;
-        // row tiles before each sequence
-        int base = 0;
-        for (int i0 = 0; i0 < a.nseq; i0 += THREADS) {
-            const int i = i0 + tid;
-            int nq = 0;
-            if (i < a.nseq) nq = (paged_seq(a, i, blockIdx.x == 0).n + a.tpt - 1) / a.tpt;
-            const int incl = base + paged_scan(nq, reinterpret_cast<int*>(sm.warp));
-            if (i < a.nseq) sm.sq[i + 1] = incl;
-            if (tid == THREADS - 1) sm.warp[15] = incl;  // THREADS / 32 <= 15, or the same value
+        if (a.nseq <= THREADS && a.max_ntok <= 4 * a.tpt) {
+            // few row tiles per sequence: a thread per sequence, one scan
+            s.n = 0;
+            int64_t cost = 0;
+            if (tid < a.nseq) {
+                const PagedSeq q = paged_seq(a, tid, blockIdx.x == 0);
+                s.seq = tid;
+                s.c = q.c;
+                s.n = q.n;
+                s.r = q.r;
+                for (qt = 0; qt * a.tpt < s.n; ++qt) cost += item(a);
+            }
+            int64_t total;
+            const int64_t incl = paged_scan<THREADS>(cost, sm.warp, total);
+            share(a, total, min_cost);
+            if (x < x_end) {
+                const int64_t y = paged_div(x, a.Hkv);
+                int64_t p = incl - cost;
+                if (p <= y && y < incl) {  // one thread's sequence
+                    qt = 0;
+                    for (int c = item(a); p + c <= y; c = item(a)) {
+                        p += c;
+                        ++qt;
+                    }
+                    place(a, p);
+                    sm.s = s;
+                    sm.qt = qt;
+                    sm.off = off;
+                }
+            }
+        } else {
+            // row tiles before each sequence
+            int base = 0;
+            for (int i0 = 0; i0 < a.nseq; i0 += THREADS) {
+                const int i = i0 + tid;
+                int nq = 0, add;
+                if (i < a.nseq) nq = (paged_seq(a, i, blockIdx.x == 0).n + a.tpt - 1) / a.tpt;
+                const int incl = base + paged_scan<THREADS>(nq, reinterpret_cast<int*>(sm.warp), add);
+                if (i < a.nseq) sm.sq[i + 1] = incl;
+                base += add;
+                __syncthreads();
+            }
+            if (tid == 0) sm.sq[0] = 0;
             __syncthreads();
-            base = (int)sm.warp[15];
+            // cost of each thread's run of row tiles
+            const int per = (base + THREADS - 1) / THREADS;
+            const int q0 = min(base, tid * per), q1 = min(base, q0 + per);
+            int64_t cost = 0, total;
+            if (q0 < q1) {
+                find(a, sm, q0);
+                for (int q = q0; q < q1; ++q) {
+                    cost += item(a);
+                    step(a);
+                }
+            }
+            const int64_t incl = paged_scan<THREADS>(cost, sm.warp, total);
+            share(a, total, min_cost);
+            if (x < x_end) {
+                const int64_t y = paged_div(x, a.Hkv);
+                int64_t p = incl - cost;
+                if (p <= y && y < incl) {  // one thread's run
+                    find(a, sm, q0);
+                    for (int c = item(a); p + c <= y; c = item(a)) {
+                        p += c;
+                        step(a);
+                    }
+                    place(a, p);
+                    sm.s = s;
+                    sm.qt = qt;
+                    sm.off = off;
+                }
+            }
         }
-        if (tid == 0) sm.sq[0] = 0;
         __syncthreads();
-        // cost of each thread's run of row tiles
-        const int per = (base + THREADS - 1) / THREADS;
-        const int q0 = min(base, tid * per), q1 = min(base, q0 + per);
-        int64_t cost = 0;
-        if (q0 < q1) {
-            find(a, sm, q0);
-            for (int q = q0; q < q1; ++q) {
-                cost += item(a);
-                step(a);
-            }
-        }
-        const int64_t incl = paged_scan(cost, sm.warp);
-        sm.tp[tid + 1] = incl;
-        if (tid == 0) sm.tp[0] = 0;
-        __syncthreads();
-        const int64_t total = sm.tp[THREADS] * a.Hkv;
-        int64_t len = (total + gridDim.x - 1) / gridDim.x;
-        len = len < min_cost ? min_cost : len;
-        x = len * blockIdx.x;
-        x_end = x + len < total ? x + len : total;
-        if (x < x_end) {
-            const int64_t y = x / a.Hkv;
-            int lo = 0, hi = THREADS;  // the last run with tp <= y
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (sm.tp[mid] <= y) lo = mid; else hi = mid;
-            }
-            int64_t p = sm.tp[lo];
-            find(a, sm, lo * per);
-            int c = item(a);
-            while (p + c <= y) {
-                p += c;
-                step(a);
-                c = item(a);
-            }
-            const int64_t rem = x - p * a.Hkv;
-            s.head = (int)(rem / c);
-            off = (int)(rem % c);
-        }
+        s = sm.s;
+        qt = sm.qt;
+        off = sm.off;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // asynchronous copies may land on `sm` next
         __syncthreads();
     }
@@ -285,13 +336,14 @@ __device__ __forceinline__ float* paged_slot(const PagedArgs& a, int cta, int sl
 }
 // A slot holds m [slot_rows] (log2 units), l [slot_rows], then O [slot_rows][d].
 
-// Adds the values of V that are not finite, of keys the row sees in key tiles that are
-// not seen whole by all rows: the kernels read such values as zeros there, because a
-// matrix product would carry them (0 * inf) into rows whose mask hides them.
-// `o`: `n` channels from channel c0.
+// The sum of the values of V in channel c that are not finite, of keys the row sees in
+// key tiles that are not seen whole by all rows (0 if there are none): the kernels read
+// such values as zeros there, because a matrix product would carry them (0 * inf) into
+// rows whose mask hides them.
 template <int KT>
-__device__ __noinline__ void paged_add_nonfinite(const PagedArgs& a, const PagedSeg& s, int pos, int c0, int n, float* o) {
+__device__ __noinline__ float paged_nonfinite(const PagedArgs& a, const PagedSeg& s, int pos, int c) {
     const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1;
+    float sum = 0.f;
     for (int t = s.ta; t < s.tb; ++t) {
         const int k0 = s.tiles.tile(t) * KT;
         if (paged_all_seen(a, k0, KT, p0, p1)) continue;
@@ -299,11 +351,9 @@ __device__ __noinline__ void paged_add_nonfinite(const PagedArgs& a, const Paged
             if (!paged_seen(a, key, pos)) continue;
             const int64_t row = paged_page(a, s.seq, key) * a.page_stride + s.head * a.head_stride +
                                 (key % a.page) * a.pos_stride;
-            const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v) + row + c0;
-            for (int i = 0; i < n; ++i) {
-                const float f = __bfloat162float(v[i]);
-                if (!isfinite(f)) o[i] += f;
-            }
+            const float f = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.v)[row + c]);
+            if (!isfinite(f)) sum += f;
         }
     }
+    return sum;
 }

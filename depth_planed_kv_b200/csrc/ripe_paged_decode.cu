@@ -330,7 +330,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
                         v[1] += f[w] * x.y;
                     }
                     const int c = half * L::HC + 2 * p;
-                    if (any_bad) paged_add_nonfinite<kKT>(a, s, s.c + s.t0 + tok, c, 2, v);
+                    if (any_bad) {
+                        v[0] += paged_nonfinite<kKT>(a, s, s.c + s.t0 + tok, c);
+                        v[1] += paged_nonfinite<kKT>(a, s, s.c + s.t0 + tok, c + 1);
+                    }
                     if (whole)
                         *reinterpret_cast<uint32_t*>(a.o + (orow * a.o_rs + (int64_t)head * D + c) * 2) =
                             pack_bf16(v[0] * inv, v[1] * inv);

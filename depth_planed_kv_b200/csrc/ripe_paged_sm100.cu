@@ -24,6 +24,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "ripe_launch.h"
 #include "ripe_paged.cuh"
 #include "ripe_paged_launch.h"
@@ -34,7 +36,8 @@ using namespace sm100;
 namespace {
 
 constexpr int kKT = 128;       // keys per tile
-constexpr int kThreads = 320;  // 8 softmax warps, the TMA warp, the MMA warp
+constexpr int kThreads = 384;  // two softmax warpgroups (warps 0-7), the MMA warp, three TMA warps
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kTmaWarps = 3;
 constexpr int kMinCost = 4;    // key tiles x M tiles a CTA takes at least (two key tiles of two M tiles)
 
 struct alignas(64) PagedMaps {
@@ -48,10 +51,12 @@ struct Lay {
     static constexpr int Q = 0;
     static constexpr int KV = 2 * TILE;
     static constexpr int BARS = KV + ST * TILE;
-    static constexpr int NBAR = 2 * ST + 2 + 2 + 2 + 2 + 4;
+    static constexpr int NBAR = 2 * ST + 2 + 2 + 2 + 2 + 2 + 2 + 4;
     static constexpr int ML = BARS + ((NBAR * 8 + 15) / 16) * 16;  // [2][128] (m, l) of stream 1
-    static constexpr int MISC = ML + 2 * 128 * 8;
+    static constexpr int SEG = ML + 2 * 128 * 8;  // the segments under way, as the TMA warp found them
+    static constexpr int MISC = SEG + 2 * 64;
     static constexpr int TOTAL = MISC + 64;
+    static_assert(sizeof(PagedSeg) <= 64, "segment slots");
     static_assert(sizeof(PagedPlanSmem) <= (size_t)ST * TILE, "plan arrays over the stages");
     static_assert(TOTAL + 512 <= 232448, "shared memory of one CTA");
 };
@@ -61,9 +66,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// The lowest n bits (all for n >= 32, none for n <= 0).
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
+// -inf where `see` has no bit.
+__device__ __forceinline__ void hide(float* v, uint32_t see) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = (see >> j) & 1 ? v[j] : -INFINITY;
+}
+
 // Zeros the values the matrix product must not see in a key tile that some row sees
 // only in part: keys from `end` on (their slots hold anything), and values that are
-// not finite (returns whether there were any; paged_add_nonfinite puts them back where
+// not finite (returns whether there were any; paged_nonfinite puts them back where
 // they are seen).  Thread t of 128 takes key t.  With two M tiles both warpgroups clean
 // the tile, each before its own product: what the later one still writes is what the
 // earlier one wrote.
@@ -113,10 +136,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     char* sKV = smem + L::KV;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
     uint64_t *kv_full = bars, *kv_empty = bars + ST, *s_full = bars + 2 * ST, *p_full = s_full + 2, *o_full = p_full + 2,
-             *o_free = o_full + 2, *q_full = o_free + 2, *q_free = q_full + 1, *ml_full = q_free + 1, *drain = ml_full + 1;
+             *o_free = o_full + 2, *q_full = o_free + 2, *q_free = q_full + 1, *ml_full = q_free + 1, *drain = ml_full + 1,
+             *seg_full = drain + 1, *seg_empty = seg_full + 2;
     float2* s_ml = reinterpret_cast<float2*>(smem + L::ML);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
+    PagedSeg* s_seg[2] = {reinterpret_cast<PagedSeg*>(smem + L::SEG), reinterpret_cast<PagedSeg*>(smem + L::SEG + 64)};
     volatile int* s_bad = reinterpret_cast<volatile int*>(smem + L::MISC + 16);  // [4] item with non-finite values
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -130,6 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             mbar_init(p_full + i, 128);
             mbar_init(o_full + i, 1);
             mbar_init(o_free + i, 128);
+            mbar_init(seg_full + i, 1);
+            mbar_init(seg_empty + i, 8 + kTmaWarps);  // all but the warp that fills it
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
@@ -139,121 +166,207 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         *abort_flag = 0;
         for (int i = 0; i < 4; ++i) s_bad[i] = 0;
     }
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         tmem_alloc(s_tmem, 512);
         tmem_relinquish();
     }
-    if (warp == 8 && lane < 3) prefetch_tmap(lane == 0 ? &tm.q : lane == 1 ? &tm.k : &tm.v);
-    PagedPlan<kKT> plan;
+    if (warp == kTmaWarp && lane < 3) prefetch_tmap(lane == 0 ? &tm.q : lane == 1 ? &tm.k : &tm.v);
+    PagedPlan<kKT> plan;  // carried on by the first TMA warp alone
     plan.template begin<kThreads>(a, *reinterpret_cast<PagedPlanSmem*>(sKV), kMinCost);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    const uint32_t S_COL[2] = {tmem, tmem + 128}, O_COL[2] = {tmem + 256, tmem + 256 + D};
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ TMA producer
-        // Lane l: box l of a tile, sub-block l / NCH of its keys (a page, or 128 keys of
-        // one), chunk l % NCH.
+    if (warp >= kTmaWarp) {
+        // ------------------------------------------------------------ TMA producers
+        // A tile is nsub (pages, or 128 keys of one) x NCH boxes, dealt to the lanes of three
+        // warps: a lane's copy takes the warp about 64 cycles to issue, so with pages of 16
+        // keys one warp alone would hold a tile back for 4100 cycles (measured: 15 bytes per
+        // cycle and SM instead of the 23 that HBM gives).
+        const int pw = warp - kTmaWarp, b = lane * kTmaWarps + pw;
         const int pb = a.page < kKT ? a.page : kKT, nsub = kKT / pb;
-        const int sub = lane / NCH, ch = lane % NCH;
+        const int sub = b / NCH, ch = b % NCH;
         const uint32_t box = (uint32_t)pb * 64;
-        PagedSeg s;
-        int it = 0, seg = 0;  // stages filled, segments begun
+        char* dst = sKV + ch * 8192 + sub * (int)box;
+        int st = 0, ph = 1, n = 0;  // stage, its empty parity (the first round passes), segments begun
         bool ok = true;
-        while (ok && plan.next(a, s)) {
-            const int end = s.c + s.t0 + s.ntok;
-            if (seg > 0 && !(ok = warp_wait(q_free, (seg - 1) & 1, abort_flag, a.err))) break;
-            if (lane == 0) {
-                const uint32_t qbox = (uint32_t)a.tok1 * a.G * 64;
-                mbar_expect_tx(q_full, s.w * NCH * qbox);
-                for (int mt = 0; mt < s.w; ++mt)
-                    for (int c = 0; c < NCH; ++c)
-                        tma_load_3d(sQ + (mt * NCH + c) * 8192, &tm.q, 32 * c, s.head * a.G, s.r + s.t0 + mt * a.tok1, q_full);
+        for (;; ++n) {
+            PagedSeg* slot = s_seg[n & 1];
+            if (pw == 0) {
+                // The next segment, for the other warps too; one without keys ends the work.
+                PagedSeg s;
+                if (!plan.next(a, s)) s.ta = s.tb = 0;
+                if (!(ok = warp_wait(seg_empty + (n & 1), ((n >> 1) & 1) ^ 1, abort_flag, a.err))) break;
+                if (lane == 0) {
+                    *slot = s;
+                    mbar_arrive(seg_full + (n & 1));
+                }
+                __syncwarp();
+            } else if (!(ok = warp_wait(seg_full + (n & 1), (n >> 1) & 1, abort_flag, a.err))) {
+                break;
             }
-            ++seg;
+            const int ta = slot->ta, tb = slot->tb;
+            if (ta == tb) break;
+            const int end = slot->c + slot->t0 + slot->ntok, head = slot->head, seq = slot->seq;
+            const PagedTiles tiles = slot->tiles;
+            if (pw == 0) {
+                if (!(ok = warp_wait(q_free, (n & 1) ^ 1, abort_flag, a.err))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(q_full, slot->w * NCH * ((uint32_t)a.tok1 * a.G * 64));
+                    for (int mt = 0; mt < slot->w; ++mt)
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_3d(sQ + (mt * NCH + c) * 8192, &tm.q, 32 * c, head * a.G,
+                                        slot->r + slot->t0 + mt * a.tok1, q_full);
+                }
+                __syncwarp();
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(seg_empty + (n & 1));
+            }
             auto page_of = [&](int t) {
-                const int key = s.tiles.tile(t) * kKT + sub * pb;
-                return t < s.tb && sub < nsub && key < end ? paged_page(a, s.seq, key) : -1;
+                const int key = tiles.tile(t) * kKT + sub * pb;
+                return t < tb && sub < nsub && key < end ? paged_page(a, seq, key) : -1;
             };
-            int id = page_of(s.ta);
-            for (int t = s.ta; t < s.tb && ok; ++t) {
+            int id = page_of(ta);
+            for (int t = ta; t < tb && ok; ++t) {
                 const int next_id = page_of(t + 1);
-                const int k0 = s.tiles.tile(t) * kKT, y = (k0 + sub * pb) % a.page;
-                const int boxes = min(nsub, (end - k0 + pb - 1) / pb) * NCH;
-                for (int kv = 0; kv < 2; ++kv, ++it) {
-                    const int st = it % ST;
-                    if (it >= ST && !(ok = warp_wait(kv_empty + st, ((it / ST) - 1) & 1, abort_flag, a.err))) break;
-                    if (lane == 0) mbar_expect_tx(kv_full + st, boxes * box);
+                const int k0 = tiles.tile(t) * kKT, y = (k0 + sub * pb) & (a.page - 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!(ok = warp_wait(kv_empty + st, ph, abort_flag, a.err))) break;
+                    if (pw == 0 && lane == 0)
+                        mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
+                    if (id >= 0) tma_load_4d(dst + st * L::TILE, kv ? &tm.v : &tm.k, 32 * ch, y, head, id, kv_full + st);
                     __syncwarp();
-                    if (lane < boxes)
-                        tma_load_4d(sKV + st * L::TILE + ch * 8192 + sub * (int)box, kv ? &tm.v : &tm.k, 32 * ch, y, s.head, id,
-                                    kv_full + st);
+                    if (++st == ST) {
+                        st = 0;
+                        ph ^= 1;
+                    }
                 }
                 id = next_id;
             }
         }
         // Every copy has landed before the CTA's shared memory goes away: on the ordinary
-        // way out the MMA warp waited for all of them.
+        // way out the MMA warp waited for all of them.  Otherwise a stage may lack the first
+        // warp's share of the bytes it expects, so give the copies time instead of waiting on it.
         if (!ok || *abort_flag) {
-            volatile int no_abort = 0;
-            if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, &no_abort, a.err);
-            for (int i = it > ST ? it - ST : 0; i < it; ++i) mbar_wait(kv_full + i % ST, (i / ST) & 1, &no_abort, a.err);
+            const long long t0 = clock64();
+            while (clock64() - t0 < (1 << 20)) {}
         }
-    } else if (warp == 9) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t IDESC_QK = idesc_bf16(128, kKT, 0), IDESC_PV = idesc_bf16(128, D, 1);
-            const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV);
-            PagedSeg s;
-            int base = 0, seg = 0, steps[2] = {0, 0}, uses[2] = {0, 0};  // stages, segments, steps and segments of a stream
+            const uint64_t dq = smem_desc(smem_u32(sQ), 16, 512, kLayoutSwizzle64B);
+            const uint64_t dk = smem_desc(smem_u32(sKV), 16, 512, kLayoutSwizzle64B);
+            const uint64_t dv = smem_desc(smem_u32(sKV), 8192, 512, kLayoutSwizzle64B);
+            int seg = 0, st0 = 0, ph0 = 0;  // the segment's first stage
+            uint32_t steps[2] = {0, 0}, uses[2] = {0, 0};
             bool ok = true;
-            while (ok && plan.next(a, s)) {
-                const int T = s.tb - s.ta, U = T * s.w;
-                auto qk = [&](int u) -> bool {
-                    const int st_i = u & 1, i = s.w == 2 ? u >> 1 : u, k = base + 2 * i, st = k % ST;
-                    if ((s.w == 1 || st_i == 0) && !mbar_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err)) return false;
-                    tc_fence_after();
-                    const uint32_t qa = q0 + (s.w == 2 ? st_i : 0) * L::TILE;
+            // stage `k` places after (st0, ph0); k < 2 * ST
+            auto at = [&](int k, int& st, uint32_t& ph) {
+                st = st0 + k;
+                ph = ph0;
+                while (st >= ST) {
+                    st -= ST;
+                    ph ^= 1;
+                }
+            };
+            // S of stream s = Q tile `qt` x K in stage st
+            auto qk = [&](auto s, int qt, int st) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t o = (ks >> 1) * 8192 + (ks & 1) * 32;
-                        mma_bf16(S_COL[st_i], smem_desc(qa + o, 16, 512, kLayoutSwizzle64B),
-                                 smem_desc(kv0 + st * L::TILE + o, 16, 512, kLayoutSwizzle64B), IDESC_QK, ks > 0 ? 1u : 0u);
-                    }
-                    mma_commit(s_full + st_i);
-                    if (s.w == 1 || st_i == 1) mma_commit(kv_empty + st);
-                    return true;
-                };
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    constexpr uint32_t u = 1;  // 16-byte units
+                    const uint32_t o = ((ks >> 1) * 8192 + (ks & 1) * 32) / 16 * u;
+                    mma_bf16(tmem + 128 * s.value, dq + qt * (L::TILE / 16) + o, dk + st * (L::TILE / 16) + o, IDESC_QK,
+                             ks > 0 ? 1u : 0u);
+                }
+                mma_commit(s_full + s.value);
+            };
+            // O of stream s += P x V in stage st; waits for P, and for O before its first use
+            auto pv = [&](auto s, bool first, int st, uint32_t ph) -> bool {
+                if (!mbar_wait(p_full + s.value, steps[s.value]++ & 1, abort_flag, a.err)) return false;
+                if (first && !mbar_wait(o_free + s.value, (uses[s.value]++ & 1) ^ 1, abort_flag, a.err)) return false;
+                if (!mbar_wait(kv_full + st, ph, abort_flag, a.err)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < kKT / 16; ++ks)
+                    mma_bf16_ts(tmem + 256 + D * s.value, tmem + 128 * s.value + ks * 8,
+                                dv + st * (L::TILE / 16) + ks * 64, IDESC_PV, (!first || ks > 0) ? 1u : 0u);
+                return true;
+            };
+            const std::integral_constant<int, 0> s0{};
+            const std::integral_constant<int, 1> s1{};
+            while ((ok = mbar_wait(seg_full + (seg & 1), (seg >> 1) & 1, abort_flag, a.err))) {
+                const PagedSeg& s = *s_seg[seg & 1];
+                const int T = s.tb - s.ta;
+                const bool two = s.w == 2;
+                mbar_arrive(seg_empty + (seg & 1));
+                if (T == 0) break;
                 if (!(ok = mbar_wait(q_full, seg & 1, abort_flag, a.err))) break;
                 ++seg;
-                for (int u = 0; u < 2 && u < U && ok; ++u) ok = qk(u);
-                if (ok && U <= 2) mma_commit(q_free);
-                for (int u = 0; u < U && ok; ++u) {
-                    const int st_i = u & 1, i = s.w == 2 ? u >> 1 : u, k = base + 2 * i + 1, st = k % ST;
-                    const bool first = u < 2;
-                    if (!(ok = mbar_wait(p_full + st_i, steps[st_i] & 1, abort_flag, a.err))) break;
-                    ++steps[st_i];
-                    if (first) {
-                        if (uses[st_i] > 0 && !(ok = mbar_wait(o_free + st_i, (uses[st_i] - 1) & 1, abort_flag, a.err))) break;
-                        ++uses[st_i];
+                int st, kst;
+                uint32_t ph, kph;
+                // stages in order: K 0, V 0, K 1, V 1, ...
+                at(0, st, ph);
+                if (!(ok = mbar_wait(kv_full + st, ph, abort_flag, a.err))) break;
+                if (two) {
+                    qk(s0, 0, st);
+                    qk(s1, 1, st);
+                    mma_commit(kv_empty + st);
+                    if (T == 1) mma_commit(q_free);
+                    for (int i = 0; i < T; ++i) {
+                        at(1, st, ph);
+                        at(2, kst, kph);
+                        const bool last = i + 1 == T;
+                        if (!(ok = pv(s0, i == 0, st, ph))) break;
+                        if (last) {
+                            mma_commit(o_full);
+                        } else {
+                            if (!(ok = mbar_wait(kv_full + kst, kph, abort_flag, a.err))) break;
+                            qk(s0, 0, kst);
+                        }
+                        if (!(ok = pv(s1, i == 0, st, ph))) break;
+                        mma_commit(kv_empty + st);
+                        if (last) {
+                            mma_commit(o_full + 1);
+                        } else {
+                            qk(s1, 1, kst);
+                            mma_commit(kv_empty + kst);
+                            if (i + 2 == T) mma_commit(q_free);
+                        }
+                        at(2, st0, kph);
+                        ph0 = kph;
                     }
-                    if ((s.w == 1 || st_i == 0) && !(ok = mbar_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int ks = 0; ks < kKT / 16; ++ks)
-                        mma_bf16_ts(O_COL[st_i], S_COL[st_i] + ks * 8,
-                                    smem_desc(kv0 + st * L::TILE + ks * 1024, 8192, 512, kLayoutSwizzle64B), IDESC_PV,
-                                    (!first || ks > 0) ? 1u : 0u);
-                    if (s.w == 1 || st_i == 1) mma_commit(kv_empty + st);
-                    if (u + 2 >= U) mma_commit(o_full + st_i);
-                    if (u + 2 < U) {
-                        ok = qk(u + 2);
-                        if (ok && u + 3 == U) mma_commit(q_free);
+                } else {
+                    qk(s0, 0, st);
+                    mma_commit(kv_empty + st);
+                    if (T > 1) {
+                        at(2, st, ph);
+                        if (!(ok = mbar_wait(kv_full + st, ph, abort_flag, a.err))) break;
+                        qk(s1, 0, st);
+                        mma_commit(kv_empty + st);
+                    }
+                    if (T <= 2) mma_commit(q_free);
+                    for (int i = 0; i < T; ++i) {
+                        at(1, st, ph);
+                        if (!(ok = i & 1 ? pv(s1, i == 1, st, ph) : pv(s0, i == 0, st, ph))) break;
+                        mma_commit(kv_empty + st);
+                        if (i + 2 < T) {
+                            at(4, kst, kph);
+                            if (!(ok = mbar_wait(kv_full + kst, kph, abort_flag, a.err))) break;
+                            if (i & 1) qk(s1, 0, kst); else qk(s0, 0, kst);
+                            mma_commit(kv_empty + kst);
+                            if (i + 3 == T) mma_commit(q_free);
+                        } else {
+                            mma_commit(o_full + (i & 1));
+                        }
+                        at(2, st0, kph);
+                        ph0 = kph;
                     }
                 }
-                base += 2 * T;
+                if (!ok) break;
             }
             // Every MMA issued so far has completed before TMEM is released.
             volatile int no_abort = 0;
@@ -265,14 +378,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         // ------------------------------------------------------------ softmax and epilogue
         const int wg = warp / 4, t = threadIdx.x % 128;  // stream; TMEM lane = row of the M tile
         const uint32_t lane_addr = (uint32_t)((warp % 4) * 32) << 16;
+        const uint32_t s_col = tmem + 128 * wg + lane_addr, o_col1 = tmem + 256 + D + lane_addr,
+                       o_col = wg ? o_col1 : tmem + 256 + lane_addr;
         const float c2 = a.scale_log2;
         const int tok = t / a.G, g = t - tok * a.G;
-        PagedSeg s;
-        int base = 0, seg = 0, steps = 0, joins = 0, uses[2] = {0, 0};  // as in the MMA warp
+        int base = 0, seg = 0, steps = 0, joins = 0, uses = 0, uses1 = 0;  // uses: of this stream, and of stream 1, as in the MMA warp
         if (threadIdx.x == 0) a.hdr[blockIdx.x].kind = 0;
         bool ok = true;
-        while (ok && plan.next(a, s)) {
+        while (ok && (ok = warp_wait(seg_full + (seg & 1), (seg >> 1) & 1, abort_flag, a.err))) {
+            const PagedSeg& s = *s_seg[seg & 1];
             const int T = s.tb - s.ta;
+            if (T == 0) break;
             const int mytok = s.t0 + (s.w == 2 ? wg * a.tok1 : 0) + tok;  // this row's token
             const bool valid = tok < a.tok1 && mytok < s.t0 + s.ntok;
             const int pos = s.c + mytok;
@@ -285,26 +401,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
                 if (!(ok = warp_wait(s_full + wg, steps & 1, abort_flag, a.err))) break;
                 tc_fence_after();
-                float v[kKT];
-#pragma unroll
-                for (int c = 0; c < kKT; c += 32) tmem_ld32(S_COL[wg] + lane_addr + c, v + c);
-                tmem_wait_ld();
+                // Two passes over S, a chunk of columns at a time: the second read costs less
+                // than holding 128 scores (tensor memory gives a warp 32 columns in about 32
+                // cycles, and a row of scores beside the rest does not fit 168 registers).
+                uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
                 if (part) {
                     // keys past the row's own position, or neither in its window nor among the first
                     const int hi = pos - k0, lo = a.window > 0 ? pos - a.window - k0 : -1, first = a.sinks - k0;
 #pragma unroll
-                    for (int c = 0; c < kKT; ++c)
-                        if (c > hi || (c <= lo && c >= first)) v[c] = -INFINITY;
+                    for (int c = 0; c < 4; ++c)
+                        see[c] = below(hi + 1 - 32 * c) & (~below(lo + 1 - 32 * c) | below(first - 32 * c));
                 }
-                float mx0 = v[0], mx1 = v[1], mx2 = v[2], mx3 = v[3];
+                float mx = -INFINITY;
 #pragma unroll
-                for (int c = 4; c < kKT; c += 4) {
-                    mx0 = fmaxf(mx0, v[c]);
-                    mx1 = fmaxf(mx1, v[c + 1]);
-                    mx2 = fmaxf(mx2, v[c + 2]);
-                    mx3 = fmaxf(mx3, v[c + 3]);
+                for (int c = 0; c < 4; c += 2) {
+                    float v[64];
+                    tmem_ld32(s_col + 32 * c, v);
+                    tmem_ld32(s_col + 32 * c + 32, v + 32);
+                    tmem_wait_ld32(v);
+                    tmem_wait_ld32(v + 32);
+                    if (part) {
+                        hide(v, see[c]);
+                        hide(v + 32, see[c + 1]);
+                    }
+                    float m0 = v[0], m1 = v[1];
+#pragma unroll
+                    for (int j = 2; j < 62; j += 4) {
+                        m0 = max3(m0, v[j], v[j + 1]);
+                        m1 = max3(m1, v[j + 2], v[j + 3]);
+                    }
+                    mx = max3(mx, max3(m0, v[62], v[63]), m1);
                 }
-                const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c2;
+                mx *= c2;
                 const bool grow = valid && mx > m + 8.f;  // m = -inf: any finite maximum
                 if (__any_sync(0xffffffffu, grow)) {
                     const float mn = grow ? mx : m;
@@ -316,23 +444,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 #pragma unroll
                         for (int c = 0; c < D; c += 32) {
                             float o[32];
-                            tmem_ld32(O_COL[wg] + lane_addr + c, o);
-                            tmem_wait_ld();
+                            tmem_ld32(o_col + c, o);
+                            tmem_wait_ld32(o);
 #pragma unroll
                             for (int j = 0; j < 32; ++j) o[j] *= f;
-                            tmem_st32(O_COL[wg] + lane_addr + c, o);
+                            tmem_st32(o_col + c, o);
                         }
                     }
                 }
                 const float mref = m == -INFINITY ? 0.f : m;
                 float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+                float v[2][32];
+                tmem_ld32(s_col, v[0]);
 #pragma unroll
-                for (int c = 0; c < kKT; c += 32) {
+                for (int c = 0; c < 4; ++c) {
+                    tmem_wait_ld32(v[c & 1]);
+                    if (c < 3) tmem_ld32(s_col + 32 * (c + 1), v[(c + 1) & 1]);
+                    float* x = v[c & 1];
+                    if (part) hide(x, see[c]);
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        const float e0 = ex2(fmaf(v[c + j], c2, -mref)), e1 = ex2(fmaf(v[c + j + 1], c2, -mref));
-                        const float e2 = ex2(fmaf(v[c + j + 2], c2, -mref)), e3 = ex2(fmaf(v[c + j + 3], c2, -mref));
+                        const float e0 = ex2(fmaf(x[j], c2, -mref)), e1 = ex2(fmaf(x[j + 1], c2, -mref));
+                        const float e2 = ex2(fmaf(x[j + 2], c2, -mref)), e3 = ex2(fmaf(x[j + 3], c2, -mref));
                         l0 += e0;
                         l1 += e1;
                         l2 += e2;
@@ -340,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         w[j / 2] = pack_bf16(e0, e1);
                         w[j / 2 + 1] = pack_bf16(e2, e3);
                     }
-                    tmem_st16(S_COL[wg] + lane_addr + c / 2, w);
+                    tmem_st16(s_col + 16 * c, w);  // over columns read before
                 }
                 l += (l0 + l1) + (l2 + l3);
                 if (part) {
@@ -375,10 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 mbar_arrive(ml_full);
             }
             if (s.w == 2 || wg == 0) {
-                if (!(ok = warp_wait(o_full + wg, uses[wg] & 1, abort_flag, a.err))) break;
+                if (!(ok = warp_wait(o_full + wg, uses & 1, abort_flag, a.err))) break;
                 if (two) {
                     if (!(ok = warp_wait(ml_full, joins & 1, abort_flag, a.err))) break;
-                    if (!(ok = warp_wait(o_full + 1, uses[1] & 1, abort_flag, a.err))) break;
+                    if (!(ok = warp_wait(o_full + 1, uses1 & 1, abort_flag, a.err))) break;
                     const float2 x = s_ml[(joins & 1) * 128 + t];
                     const float mn = fmaxf(m, x.x);
                     f0 = m == mn ? 1.f : ex2(m - mn);
@@ -402,22 +536,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
-                    tmem_ld32(O_COL[wg] + lane_addr + c, o);
+                    tmem_ld32(o_col + c, o);
                     if (two) {
                         float o1[32];
-                        tmem_ld32(O_COL[1] + lane_addr + c, o1);
-                        tmem_wait_ld();
+                        tmem_ld32(o_col1 + c, o1);
+                        tmem_wait_ld32(o);
+                        tmem_wait_ld32(o1);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + o1[j] * f1;
                     } else {
-                        tmem_wait_ld();
+                        tmem_wait_ld32(o);
                     }
                     if (c + 32 == D) {
                         tc_fence_before();
                         mbar_arrive(o_free + wg);
                         if (two) mbar_arrive(o_free + 1);
                     }
-                    if (bad && valid) paged_add_nonfinite<kKT>(a, s, pos, c, 32, o);
                     if (valid && whole) {
                         uint4* dst = reinterpret_cast<uint4*>(a.o + (row * a.o_rs + (int64_t)head * D + c) * 2);
 #pragma unroll
@@ -425,17 +559,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             dst[j / 8] = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
                                                     pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
                     } else if (valid) {
-                        float2* dst = reinterpret_cast<float2*>(part + 2 * a.slot_rows + (int64_t)prow * D + c);
+                        float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows + (int64_t)prow * D + c);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) dst[j / 2] = make_float2(o[j], o[j + 1]);
+                        for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                     __syncwarp();
                 }
+                if (bad && valid) {  // onto what this thread has just written
+                    for (int c = 0; c < D; ++c) {
+                        const float x = paged_nonfinite<kKT>(a, s, pos, c);
+                        if (x == 0.f) continue;
+                        __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(a.o) + row * a.o_rs + (int64_t)head * D + c;
+                        if (whole) *at = __float2bfloat16_rn(__bfloat162float(*at) + x);
+                        else part[2 * a.slot_rows + (int64_t)prow * D + c] += x;
+                    }
+                }
             }
-            uses[0] += 1;
-            uses[1] += s.w == 2 || two;
+            uses1 += s.w == 2 || two;
+            uses = wg ? uses1 : uses + 1;
             joins += two;
             base += 2 * T;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(seg_empty + (seg & 1));
             ++seg;
         }
     }
@@ -444,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

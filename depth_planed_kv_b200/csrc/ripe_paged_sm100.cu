@@ -63,7 +63,7 @@ struct Lay {
 
 // Waits with the whole warp: true only if every lane saw the phase complete.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+    return __all_sync(0xffffffffu, mbar_wait_idle(bar, parity, abort, err));
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -76,53 +76,156 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// Exponential and packing that stay where they are written.
+__device__ __forceinline__ float ex2_here(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_here(float lo, float hi) {
+    uint32_t y;
+    asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
 // The lowest n bits (all for n >= 32, none for n <= 0).
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 // -inf where `see` has no bit.
 __device__ __forceinline__ void hide(float* v, uint32_t see) {
+    if (__all_sync(0xffffffffu, see == ~0u)) return;
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = (see >> j) & 1 ? v[j] : -INFINITY;
 }
 
 // Zeros the values the matrix product must not see in a key tile that some row sees
-// only in part: keys from `end` on (their slots hold anything), and values that are
-// not finite (returns whether there were any; paged_nonfinite puts them back where
-// they are seen).  Thread t of 128 takes key t.  With two M tiles both warpgroups clean
-// the tile, each before its own product: what the later one still writes is what the
-// earlier one wrote.
+// only in part: keys from `end` (of the tile) on, whose slots hold anything, and values
+// that are not finite (returns whether there were any; paged_nonfinite puts them back
+// where they are seen).  128 threads, 16 bytes at a time in the order they lie.  With two
+// M tiles both warpgroups clean the tile, each before its own product: what the later one
+// still writes is what the earlier one wrote.
 template <int NCH>
-__device__ __forceinline__ bool clean_values(char* sv, int t, bool past) {
+__device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
     bool found = false;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-        uint4* row = reinterpret_cast<uint4*>(sv + c * 8192 + t * 64);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint4 x = row[i];
-            if (past) {
-                if (x.x | x.y | x.z | x.w) row[i] = make_uint4(0, 0, 0, 0);
-                continue;
-            }
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            bool bad = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if ((w[j] & 0x7F80u) == 0x7F80u) {
-                    w[j] &= 0xFFFF0000u;
-                    bad = true;
-                }
-                if ((w[j] & 0x7F800000u) == 0x7F800000u) {
-                    w[j] &= 0xFFFFu;
-                    bad = true;
-                }
-            }
-            if (bad) {
-                row[i] = x;
-                found = true;
-            }
+#pragma unroll 4
+    for (int i = t; i < NCH * 512; i += 128) {
+        uint4* at = reinterpret_cast<uint4*>(sv) + i;
+        uint4 x = *at;
+        if (((i & 511) >> 2) >= end) {  // four 16-byte units a key
+            if (x.x | x.y | x.z | x.w) *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        // an exponent of all ones carries into its sign bit
+        auto top = [](uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+        if (top(x.x) | top(x.y) | top(x.z) | top(x.w)) {
+            auto finite = [&](uint32_t w) {
+                const uint32_t b = top(w);
+                return w & ~((b >> 15 & 1u) * 0x0000FFFFu | (b >> 31) * 0xFFFF0000u);
+            };
+            *at = make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w));
+            found = true;
         }
     }
     return found;
+}
+
+// One key tile of one row: S (128 columns at s_col) -> P over it, the running maximum m
+// (log2 units) and sum l, and O (at o_col) rescaled where the maximum moved.  PART: keys
+// past `hi`, or up to `lo` and not below `first` (all from the tile's first key), are
+// hidden.  Two code paths, because the test alone costs the full tiles a third of their
+// time once the compiler turns it into selects.
+template <int D, bool PART>
+__device__ __forceinline__ void softmax_step(uint32_t s_col, uint32_t o_col, float c2, int hi, int lo,
+                                             int first, bool valid, bool have_o, float& m, float& l) {
+    // Two passes over S, a chunk of columns at a time: the second read costs less
+    // than holding 128 scores (tensor memory gives a warp 32 columns in about 32
+    // cycles, and a row of scores beside the rest does not fit 168 registers).
+    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+    if (PART) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            see[c] = below(hi + 1 - 32 * c) & (~below(lo + 1 - 32 * c) | below(first - 32 * c));
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 4; c += 2) {
+        float v[64];
+        tmem_ld32(s_col + 32 * c, v);
+        tmem_ld32(s_col + 32 * c + 32, v + 32);
+        tmem_wait_ld32(v);
+        tmem_wait_ld32(v + 32);
+        if (PART) {
+            hide(v, see[c]);
+            hide(v + 32, see[c + 1]);
+        }
+        float m0 = v[0], m1 = v[1];
+#pragma unroll
+        for (int j = 2; j < 62; j += 4) {
+            m0 = max3(m0, v[j], v[j + 1]);
+            m1 = max3(m1, v[j + 2], v[j + 3]);
+        }
+        mx = max3(mx, max3(m0, v[62], v[63]), m1);
+    }
+    mx *= c2;
+    const bool grow = valid && mx > m + 8.f;  // m = -inf: any finite maximum
+    if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? mx : m;
+        const float f = m == mn ? 1.f : ex2(m - mn);  // 0 from m = -inf
+        m = mn;
+        l *= f;
+        if (have_o) {
+            // The stream's earlier P V are complete: s_full came after them.
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(o_col + c, o);
+                tmem_wait_ld32(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] *= f;
+                tmem_st32(o_col + c, o);
+            }
+        }
+    }
+    const float mref = m == -INFINITY ? 0.f : m;
+    // Exponentials of chunk c while chunk c - 1 is summed and packed: written out in
+    // that order (the asm statements keep it), because the exponential unit takes a
+    // warp 8 cycles an instruction and a warp that waits for each result idles it.
+    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+    float v[3][32];
+    tmem_ld32(s_col, v[0]);
+#pragma unroll
+    for (int c = 0; c <= 4; ++c) {
+        float *x = v[c % 3], *y = v[(c + 2) % 3];
+        uint32_t w[16];
+        if (c < 4) {
+            tmem_wait_ld32(x);
+            if (c < 3) tmem_ld32(s_col + 32 * (c + 1), v[(c + 1) % 3]);
+            if (PART) hide(x, see[c]);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = fmaf(x[j], c2, -mref);
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            if (c < 4) {
+                x[j] = ex2_here(x[j]);
+                x[j + 1] = ex2_here(x[j + 1]);
+            }
+            if (c > 0) {
+                l0 += y[j];
+                l1 += y[j + 1];
+                w[j / 2] = pack_here(y[j], y[j + 1]);
+            }
+            if (c < 4) {
+                x[j + 2] = ex2_here(x[j + 2]);
+                x[j + 3] = ex2_here(x[j + 3]);
+            }
+            if (c > 0) {
+                l2 += y[j + 2];
+                l3 += y[j + 3];
+                w[j / 2 + 1] = pack_here(y[j + 2], y[j + 3]);
+            }
+        }
+        if (c > 0) tmem_st16(s_col + 16 * (c - 1), w);  // over columns read before
+    }
+    l += (l0 + l1) + (l2 + l3);
 }
 
 template <int D, int ST>
@@ -286,9 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             };
             // O of stream s += P x V in stage st; waits for P, and for O before its first use
             auto pv = [&](auto s, bool first, int st, uint32_t ph) -> bool {
-                if (!mbar_wait(p_full + s.value, steps[s.value]++ & 1, abort_flag, a.err)) return false;
-                if (first && !mbar_wait(o_free + s.value, (uses[s.value]++ & 1) ^ 1, abort_flag, a.err)) return false;
-                if (!mbar_wait(kv_full + st, ph, abort_flag, a.err)) return false;
+                if (!mbar_wait_idle(p_full + s.value, steps[s.value]++ & 1, abort_flag, a.err)) return false;
+                if (first && !mbar_wait_idle(o_free + s.value, (uses[s.value]++ & 1) ^ 1, abort_flag, a.err)) return false;
+                if (!mbar_wait_idle(kv_full + st, ph, abort_flag, a.err)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kKT / 16; ++ks)
@@ -298,19 +401,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             };
             const std::integral_constant<int, 0> s0{};
             const std::integral_constant<int, 1> s1{};
-            while ((ok = mbar_wait(seg_full + (seg & 1), (seg >> 1) & 1, abort_flag, a.err))) {
+            while ((ok = mbar_wait_idle(seg_full + (seg & 1), (seg >> 1) & 1, abort_flag, a.err))) {
                 const PagedSeg& s = *s_seg[seg & 1];
                 const int T = s.tb - s.ta;
                 const bool two = s.w == 2;
                 mbar_arrive(seg_empty + (seg & 1));
                 if (T == 0) break;
-                if (!(ok = mbar_wait(q_full, seg & 1, abort_flag, a.err))) break;
+                if (!(ok = mbar_wait_idle(q_full, seg & 1, abort_flag, a.err))) break;
                 ++seg;
                 int st, kst;
                 uint32_t ph, kph;
                 // stages in order: K 0, V 0, K 1, V 1, ...
                 at(0, st, ph);
-                if (!(ok = mbar_wait(kv_full + st, ph, abort_flag, a.err))) break;
+                if (!(ok = mbar_wait_idle(kv_full + st, ph, abort_flag, a.err))) break;
                 if (two) {
                     qk(s0, 0, st);
                     qk(s1, 1, st);
@@ -324,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         if (last) {
                             mma_commit(o_full);
                         } else {
-                            if (!(ok = mbar_wait(kv_full + kst, kph, abort_flag, a.err))) break;
+                            if (!(ok = mbar_wait_idle(kv_full + kst, kph, abort_flag, a.err))) break;
                             qk(s0, 0, kst);
                         }
                         if (!(ok = pv(s1, i == 0, st, ph))) break;
@@ -344,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     mma_commit(kv_empty + st);
                     if (T > 1) {
                         at(2, st, ph);
-                        if (!(ok = mbar_wait(kv_full + st, ph, abort_flag, a.err))) break;
+                        if (!(ok = mbar_wait_idle(kv_full + st, ph, abort_flag, a.err))) break;
                         qk(s1, 0, st);
                         mma_commit(kv_empty + st);
                     }
@@ -355,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         mma_commit(kv_empty + st);
                         if (i + 2 < T) {
                             at(4, kst, kph);
-                            if (!(ok = mbar_wait(kv_full + kst, kph, abort_flag, a.err))) break;
+                            if (!(ok = mbar_wait_idle(kv_full + kst, kph, abort_flag, a.err))) break;
                             if (i & 1) qk(s1, 0, kst); else qk(s0, 0, kst);
                             mma_commit(kv_empty + kst);
                             if (i + 3 == T) mma_commit(q_free);
@@ -371,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             // Every MMA issued so far has completed before TMEM is released.
             volatile int no_abort = 0;
             mma_commit(drain);
-            mbar_wait(drain, 0, &no_abort, a.err);
+            mbar_wait_idle(drain, 0, &no_abort, a.err);
         }
         __syncwarp();
     } else {
@@ -399,93 +502,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int i = s.w == 2 ? n : 2 * n + wg;
                 const int k0 = s.tiles.tile(s.ta + i) * kKT;
                 const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
-                if (!(ok = warp_wait(s_full + wg, steps & 1, abort_flag, a.err))) break;
-                tc_fence_after();
-                // Two passes over S, a chunk of columns at a time: the second read costs less
-                // than holding 128 scores (tensor memory gives a warp 32 columns in about 32
-                // cycles, and a row of scores beside the rest does not fit 168 registers).
-                uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-                if (part) {
-                    // keys past the row's own position, or neither in its window nor among the first
-                    const int hi = pos - k0, lo = a.window > 0 ? pos - a.window - k0 : -1, first = a.sinks - k0;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        see[c] = below(hi + 1 - 32 * c) & (~below(lo + 1 - 32 * c) | below(first - 32 * c));
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; c += 2) {
-                    float v[64];
-                    tmem_ld32(s_col + 32 * c, v);
-                    tmem_ld32(s_col + 32 * c + 32, v + 32);
-                    tmem_wait_ld32(v);
-                    tmem_wait_ld32(v + 32);
-                    if (part) {
-                        hide(v, see[c]);
-                        hide(v + 32, see[c + 1]);
-                    }
-                    float m0 = v[0], m1 = v[1];
-#pragma unroll
-                    for (int j = 2; j < 62; j += 4) {
-                        m0 = max3(m0, v[j], v[j + 1]);
-                        m1 = max3(m1, v[j + 2], v[j + 3]);
-                    }
-                    mx = max3(mx, max3(m0, v[62], v[63]), m1);
-                }
-                mx *= c2;
-                const bool grow = valid && mx > m + 8.f;  // m = -inf: any finite maximum
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float mn = grow ? mx : m;
-                    const float f = m == mn ? 1.f : ex2(m - mn);  // 0 from m = -inf
-                    m = mn;
-                    l *= f;
-                    if (n > 0) {
-                        // The stream's earlier P V are complete: s_full came after them.
-#pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            float o[32];
-                            tmem_ld32(o_col + c, o);
-                            tmem_wait_ld32(o);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= f;
-                            tmem_st32(o_col + c, o);
-                        }
-                    }
-                }
-                const float mref = m == -INFINITY ? 0.f : m;
-                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-                float v[2][32];
-                tmem_ld32(s_col, v[0]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_wait_ld32(v[c & 1]);
-                    if (c < 3) tmem_ld32(s_col + 32 * (c + 1), v[(c + 1) & 1]);
-                    float* x = v[c & 1];
-                    if (part) hide(x, see[c]);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float e0 = ex2(fmaf(x[j], c2, -mref)), e1 = ex2(fmaf(x[j + 1], c2, -mref));
-                        const float e2 = ex2(fmaf(x[j + 2], c2, -mref)), e3 = ex2(fmaf(x[j + 3], c2, -mref));
-                        l0 += e0;
-                        l1 += e1;
-                        l2 += e2;
-                        l3 += e3;
-                        w[j / 2] = pack_bf16(e0, e1);
-                        w[j / 2 + 1] = pack_bf16(e2, e3);
-                    }
-                    tmem_st16(s_col + 16 * c, w);  // over columns read before
-                }
-                l += (l0 + l1) + (l2 + l3);
-                if (part) {
+                if (part) {  // while the scores are on their way
                     const int k = base + 2 * i + 1, st = k % ST;
                     if (!(ok = warp_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
-                    if (clean_values<NCH>(sKV + st * L::TILE, t, k0 + t > p1)) {
+                    if (clean_values<NCH>(sKV + st * L::TILE, t, p1 + 1 - k0)) {
                         s_bad[seg & 3] = seg + 1;
                         __threadfence_block();
                     }
                     fence_proxy_async_smem();
+                    __syncwarp();
                 }
+                if (!(ok = warp_wait(s_full + wg, steps & 1, abort_flag, a.err))) break;
+                tc_fence_after();
+                if (part)
+                    softmax_step<D, true>(s_col, o_col, c2, pos - k0, a.window > 0 ? pos - a.window - k0 : -1,
+                                          a.sinks - k0, valid, n > 0, m, l);
+                else
+                    softmax_step<D, false>(s_col, o_col, c2, 0, 0, 0, valid, n > 0, m, l);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full + wg);

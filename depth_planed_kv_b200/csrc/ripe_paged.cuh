@@ -127,7 +127,7 @@ struct PagedSeg {
 
 struct PagedPlanSmem {
     int sq[kPagedMaxSeqs + 1];  // row tiles before each sequence
-    int64_t warp[17];
+    int64_t warp[32];
     PagedSeg s;                 // where the CTA's stretch begins, as one thread finds it
     int qt, off;
 };
@@ -199,7 +199,7 @@ struct PagedPlan {
     // All threads of the block; `sm` may be reused after the call (it ends with a barrier).
     template <int THREADS>
     __device__ void begin(const PagedArgs& a, PagedPlanSmem& sm, int min_cost) {
-        static_assert(THREADS <= 512, "one run of row tiles per thread");
+        static_assert(THREADS <= 1024, "one scan value per warp");
         const int tid = threadIdx.x;
         if (a.nseq <= THREADS && a.max_ntok <= 4 * a.tpt) {
             // few row tiles per sequence: a thread per sequence, one scan

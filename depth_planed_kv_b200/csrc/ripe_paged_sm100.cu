@@ -36,8 +36,8 @@ using namespace sm100;
 namespace {
 
 constexpr int kKT = 128;       // keys per tile
-constexpr int kThreads = 384;  // two softmax warpgroups (warps 0-7), the MMA warp, three TMA warps
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kTmaWarps = 3;
+constexpr int kThreads = 640;  // softmax warps 0-15 (8 a stream), the MMA warp, three TMA warps
+constexpr int kMmaWarp = 16, kTmaWarp = 17, kTmaWarps = 3;
 constexpr int kMinCost = 4;    // key tiles x M tiles a CTA takes at least (two key tiles of two M tiles)
 
 struct alignas(64) PagedMaps {
@@ -51,9 +51,10 @@ struct Lay {
     static constexpr int Q = 0;
     static constexpr int KV = 2 * TILE;
     static constexpr int BARS = KV + ST * TILE;
-    static constexpr int NBAR = 2 * ST + 2 + 2 + 2 + 2 + 2 + 2 + 4;
-    static constexpr int ML = BARS + ((NBAR * 8 + 15) / 16) * 16;  // [2][128] (m, l) of stream 1
-    static constexpr int SEG = ML + 2 * 128 * 8;  // the segments under way, as the TMA warp found them
+    static constexpr int NBAR = 2 * ST + 7 * 2 + 3 + 16;
+    static constexpr int MX = BARS + ((NBAR * 8 + 15) / 16) * 16;  // [stream][half][128] maximum of a row's half
+    static constexpr int ML = MX + 4 * 128 * 4;                    // [2][stream][half][128] l at an item's end, then [2][128] m of stream 1
+    static constexpr int SEG = ML + 10 * 128 * 4;  // the segments under way, as the TMA warp found them
     static constexpr int MISC = SEG + 2 * 64;
     static constexpr int TOTAL = MISC + 64;
     static_assert(sizeof(PagedSeg) <= 64, "segment slots");
@@ -90,23 +91,25 @@ __device__ __forceinline__ uint32_t pack_here(float lo, float hi) {
 // The lowest n bits (all for n >= 32, none for n <= 0).
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 // -inf where `see` has no bit.
+template <int N>
 __device__ __forceinline__ void hide(float* v, uint32_t see) {
-    if (__all_sync(0xffffffffu, see == ~0u)) return;
+    constexpr uint32_t kAll = N == 32 ? ~0u : (1u << N) - 1;
+    if (__all_sync(0xffffffffu, (see & kAll) == kAll)) return;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = (see >> j) & 1 ? v[j] : -INFINITY;
+    for (int j = 0; j < N; ++j) v[j] = (see >> j) & 1 ? v[j] : -INFINITY;
 }
 
 // Zeros the values the matrix product must not see in a key tile that some row sees
 // only in part: keys from `end` (of the tile) on, whose slots hold anything, and values
 // that are not finite (returns whether there were any; paged_nonfinite puts them back
-// where they are seen).  128 threads, 16 bytes at a time in the order they lie.  With two
-// M tiles both warpgroups clean the tile, each before its own product: what the later one
+// where they are seen).  256 threads, 16 bytes at a time in the order they lie.  With two
+// M tiles both streams clean the tile, each before its own product: what the later one
 // still writes is what the earlier one wrote.
 template <int NCH>
 __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
     bool found = false;
 #pragma unroll 4
-    for (int i = t; i < NCH * 512; i += 128) {
+    for (int i = t; i < NCH * 512; i += 256) {
         uint4* at = reinterpret_cast<uint4*>(sv) + i;
         uint4 x = *at;
         if (((i & 511) >> 2) >= end) {  // four 16-byte units a key
@@ -127,44 +130,49 @@ __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
     return found;
 }
 
-// One key tile of one row: S (128 columns at s_col) -> P over it, the running maximum m
-// (log2 units) and sum l, and O (at o_col) rescaled where the maximum moved.  PART: keys
-// past `hi`, or up to `lo` and not below `first` (all from the tile's first key), are
-// hidden.  Two code paths, because the test alone costs the full tiles a third of their
-// time once the compiler turns it into selects.
+// Half a key tile of one row: S (64 columns at s_col) -> P over its first 32 columns, the
+// running maximum m (log2 units; the whole row's, the other half's warp tells its own
+// through `mx_mine`/`mx_other`) and this half's sum l, and half of O (D/2 columns at
+// o_col) rescaled where the maximum moved.  PART: keys past `hi`, or up to `lo` and not
+// below `first` (from the first of the 64), are hidden.  Two code paths, because the test
+// alone costs the full tiles a third of their time once the compiler turns it into
+// selects.  False if the wait for the other half gave up.
 template <int D, bool PART>
-__device__ __forceinline__ void softmax_step(uint32_t s_col, uint32_t o_col, float c2, int hi, int lo,
-                                             int first, bool valid, bool have_o, float& m, float& l) {
-    // Two passes over S, a chunk of columns at a time: the second read costs less
-    // than holding 128 scores (tensor memory gives a warp 32 columns in about 32
-    // cycles, and a row of scores beside the rest does not fit 168 registers).
-    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+__device__ __forceinline__ bool softmax_step(uint32_t s_col, uint32_t o_col, float c2, int hi, int lo, int first, bool valid,
+                                             bool have_o, float& m, float& l, float* mx_mine, volatile float* mx_other,
+                                             uint64_t* bar_mine, uint64_t* bar_other, uint32_t parity, int lane,
+                                             volatile int* abort, int32_t* err) {
+    // Two passes over S: the second read costs less than holding the scores.
+    uint32_t see[2] = {~0u, ~0u};
     if (PART) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
             see[c] = below(hi + 1 - 32 * c) & (~below(lo + 1 - 32 * c) | below(first - 32 * c));
     }
-    float mx = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < 4; c += 2) {
-        float v[64];
-        tmem_ld32(s_col + 32 * c, v);
-        tmem_ld32(s_col + 32 * c + 32, v + 32);
-        tmem_wait_ld32(v);
-        tmem_wait_ld32(v + 32);
+    float mx;
+    {
+        float x[32], y[32];
+        tmem_ld32(s_col, x);
+        tmem_ld32(s_col + 32, y);
+        tmem_wait_ld32(x);
+        tmem_wait_ld32(y);
         if (PART) {
-            hide(v, see[c]);
-            hide(v + 32, see[c + 1]);
+            hide<32>(x, see[0]);
+            hide<32>(y, see[1]);
         }
-        float m0 = v[0], m1 = v[1];
+        float m0 = x[0], m1 = y[0];
 #pragma unroll
-        for (int j = 2; j < 62; j += 4) {
-            m0 = max3(m0, v[j], v[j + 1]);
-            m1 = max3(m1, v[j + 2], v[j + 3]);
+        for (int j = 1; j < 31; j += 2) {
+            m0 = max3(m0, x[j], x[j + 1]);
+            m1 = max3(m1, y[j], y[j + 1]);
         }
-        mx = max3(mx, max3(m0, v[62], v[63]), m1);
+        mx = fmaxf(max3(m0, x[31], y[31]), m1);
     }
-    mx *= c2;
+    *mx_mine = mx;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_other);
+    if (!__all_sync(0xffffffffu, mbar_wait_idle(bar_mine, parity, abort, err))) return false;
+    mx = fmaxf(mx, *mx_other) * c2;
     const bool grow = valid && mx > m + 8.f;  // m = -inf: any finite maximum
     if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? mx : m;
@@ -174,13 +182,13 @@ __device__ __forceinline__ void softmax_step(uint32_t s_col, uint32_t o_col, flo
         if (have_o) {
             // The stream's earlier P V are complete: s_full came after them.
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(o_col + c, o);
-                tmem_wait_ld32(o);
+            for (int c = 0; c < D / 2; c += 16) {
+                float o[16];
+                tmem_ld16(o_col + c, o);
+                tmem_wait_ld16(o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] *= f;
-                tmem_st32(o_col + c, o);
+                for (int j = 0; j < 16; ++j) o[j] *= f;
+                tmem_st16(o_col + c, reinterpret_cast<const uint32_t*>(o));
             }
         }
     }
@@ -188,44 +196,34 @@ __device__ __forceinline__ void softmax_step(uint32_t s_col, uint32_t o_col, flo
     // Exponentials of chunk c while chunk c - 1 is summed and packed: written out in
     // that order (the asm statements keep it), because the exponential unit takes a
     // warp 8 cycles an instruction and a warp that waits for each result idles it.
-    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-    float v[3][32];
-    tmem_ld32(s_col, v[0]);
+    float l0 = 0.f, l1 = 0.f;
+    float v[3][16];
+    tmem_ld16(s_col, v[0]);
 #pragma unroll
     for (int c = 0; c <= 4; ++c) {
         float *x = v[c % 3], *y = v[(c + 2) % 3];
-        uint32_t w[16];
+        uint32_t w[8];
         if (c < 4) {
-            tmem_wait_ld32(x);
-            if (c < 3) tmem_ld32(s_col + 32 * (c + 1), v[(c + 1) % 3]);
-            if (PART) hide(x, see[c]);
+            tmem_wait_ld16(x);
+            if (c < 3) tmem_ld16(s_col + 16 * (c + 1), v[(c + 1) % 3]);
+            if (PART) hide<16>(x, see[c / 2] >> (c % 2 * 16));
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = fmaf(x[j], c2, -mref);
+            for (int j = 0; j < 16; ++j) x[j] = fmaf(x[j], c2, -mref);
         }
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            if (c < 4) {
-                x[j] = ex2_here(x[j]);
-                x[j + 1] = ex2_here(x[j + 1]);
-            }
+        for (int j = 0; j < 16; j += 2) {
+            if (c < 4) x[j] = ex2_here(x[j]);
             if (c > 0) {
                 l0 += y[j];
                 l1 += y[j + 1];
-                w[j / 2] = pack_here(y[j], y[j + 1]);
             }
-            if (c < 4) {
-                x[j + 2] = ex2_here(x[j + 2]);
-                x[j + 3] = ex2_here(x[j + 3]);
-            }
-            if (c > 0) {
-                l2 += y[j + 2];
-                l3 += y[j + 3];
-                w[j / 2 + 1] = pack_here(y[j + 2], y[j + 3]);
-            }
+            if (c < 4) x[j + 1] = ex2_here(x[j + 1]);
+            if (c > 0) w[j / 2] = pack_here(y[j], y[j + 1]);
         }
-        if (c > 0) tmem_st16(s_col + 16 * (c - 1), w);  // over columns read before
+        if (c > 0) tmem_st8(s_col + 8 * (c - 1), w);  // over columns read before
     }
-    l += (l0 + l1) + (l2 + l3);
+    l += l0 + l1;
+    return true;
 }
 
 template <int D, int ST>
@@ -239,9 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     char* sKV = smem + L::KV;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
     uint64_t *kv_full = bars, *kv_empty = bars + ST, *s_full = bars + 2 * ST, *p_full = s_full + 2, *o_full = p_full + 2,
-             *o_free = o_full + 2, *q_full = o_free + 2, *q_free = q_full + 1, *ml_full = q_free + 1, *drain = ml_full + 1,
-             *seg_full = drain + 1, *seg_empty = seg_full + 2;
-    float2* s_ml = reinterpret_cast<float2*>(smem + L::ML);
+             *o_free = o_full + 2, *seg_full = o_free + 2, *seg_empty = seg_full + 2, *ml_full = seg_empty + 2, *q_full = ml_full + 2,
+             *q_free = q_full + 1, *drain = q_free + 1, *mx_full = drain + 1;
+    float* s_mx = reinterpret_cast<float*>(smem + L::MX);
+    float *s_l = reinterpret_cast<float*>(smem + L::ML), *s_m1 = s_l + 8 * 128;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
     PagedSeg* s_seg[2] = {reinterpret_cast<PagedSeg*>(smem + L::SEG), reinterpret_cast<PagedSeg*>(smem + L::SEG + 64)};
@@ -255,15 +254,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 128);
+            mbar_init(p_full + i, 256);
             mbar_init(o_full + i, 1);
-            mbar_init(o_free + i, 128);
+            mbar_init(o_free + i, 256);
+            mbar_init(ml_full + i, 256);
             mbar_init(seg_full + i, 1);
-            mbar_init(seg_empty + i, 8 + kTmaWarps);  // all but the warp that fills it
+            mbar_init(seg_empty + i, 16 + kTmaWarps);  // all but the warp that fills it
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
-        mbar_init(ml_full, 128);
+        for (int i = 0; i < 16; ++i) mbar_init(mx_full + i, 1);
         mbar_init(drain, 1);
         fence_barrier_init();
         *abort_flag = 0;
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kKT / 16; ++ks)
-                    mma_bf16_ts(tmem + 256 + D * s.value, tmem + 128 * s.value + ks * 8,
+                    mma_bf16_ts(tmem + 256 + D * s.value, tmem + 128 * s.value + (ks & 3) * 8 + (ks >> 2) * 64,
                                 dv + st * (L::TILE / 16) + ks * 64, IDESC_PV, (!first || ks > 0) ? 1u : 0u);
                 return true;
             };
@@ -479,13 +479,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue
-        const int wg = warp / 4, t = threadIdx.x % 128;  // stream; TMEM lane = row of the M tile
+        // Warp: stream warp / 8, columns (of S and of O) of half (warp / 4) % 2, rows of
+        // quarter warp % 4.  Two warps a row, because one warp per scheduler and stream left
+        // the exponential unit half idle (2600 cycles a tile against 1060 at its rate).
+        const int wg = warp / 8, half = (warp / 4) % 2, t = threadIdx.x % 128;  // t: TMEM lane = row of the M tile
         const uint32_t lane_addr = (uint32_t)((warp % 4) * 32) << 16;
-        const uint32_t s_col = tmem + 128 * wg + lane_addr, o_col1 = tmem + 256 + D + lane_addr,
-                       o_col = wg ? o_col1 : tmem + 256 + lane_addr;
+        const uint32_t s_col = tmem + 128 * wg + 64 * half + lane_addr, o_col1 = tmem + 256 + D + D / 2 * half + lane_addr,
+                       o_col = wg ? o_col1 : o_col1 - D;
+        float* mx_mine = s_mx + (wg * 2 + half) * 128 + t;
+        float* mx_other = s_mx + (wg * 2 + (half ^ 1)) * 128 + t;
         const float c2 = a.scale_log2;
         const int tok = t / a.G, g = t - tok * a.G;
-        int base = 0, seg = 0, steps = 0, joins = 0, uses = 0, uses1 = 0;  // uses: of this stream, and of stream 1, as in the MMA warp
+        int base = 0, seg = 0, steps = 0, uses = 0, uses1 = 0;  // uses: of this stream, and of stream 1, as in the MMA warp
         if (threadIdx.x == 0) a.hdr[blockIdx.x].kind = 0;
         bool ok = true;
         while (ok && (ok = warp_wait(seg_full + (seg & 1), (seg >> 1) & 1, abort_flag, a.err))) {
@@ -502,23 +507,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int i = s.w == 2 ? n : 2 * n + wg;
                 const int k0 = s.tiles.tile(s.ta + i) * kKT;
                 const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
-                if (part) {  // while the scores are on their way
+                if (!(ok = warp_wait(s_full + wg, steps & 1, abort_flag, a.err))) break;
+                tc_fence_after();
+                if (part) {
+                    // Only once the scores are there: they come after the products that used
+                    // the stage before, so the parity cannot be that of an earlier round.
                     const int k = base + 2 * i + 1, st = k % ST;
                     if (!(ok = warp_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
-                    if (clean_values<NCH>(sKV + st * L::TILE, t, p1 + 1 - k0)) {
+                    if (clean_values<NCH>(sKV + st * L::TILE, threadIdx.x % 256, p1 + 1 - k0)) {
                         s_bad[seg & 3] = seg + 1;
                         __threadfence_block();
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (!(ok = warp_wait(s_full + wg, steps & 1, abort_flag, a.err))) break;
-                tc_fence_after();
+                const int kh = k0 + 64 * half;
                 if (part)
-                    softmax_step<D, true>(s_col, o_col, c2, pos - k0, a.window > 0 ? pos - a.window - k0 : -1,
-                                          a.sinks - k0, valid, n > 0, m, l);
+                    ok = softmax_step<D, true>(s_col, o_col, c2, pos - kh, a.window > 0 ? pos - a.window - kh : -1,
+                                               a.sinks - kh, valid, n > 0, m, l, mx_mine, mx_other, mx_full + warp,
+                                               mx_full + (warp ^ 4), steps & 1, lane, abort_flag, a.err);
                 else
-                    softmax_step<D, false>(s_col, o_col, c2, 0, 0, 0, valid, n > 0, m, l);
+                    ok = softmax_step<D, false>(s_col, o_col, c2, 0, 0, 0, valid, n > 0, m, l, mx_mine, mx_other,
+                                                mx_full + warp, mx_full + (warp ^ 4), steps & 1, lane, abort_flag, a.err);
+                if (!ok) break;
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_full + wg);
@@ -535,23 +546,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 h.head = s.head;
                 a.hdr[blockIdx.x] = h;
             }
-            float f0 = 1.f, f1 = 0.f;
             const bool two = s.w == 1 && T > 1;  // both streams hold a part of the one M tile
-            if (two && wg == 1) {
-                s_ml[(joins & 1) * 128 + t] = make_float2(m, l);
-                mbar_arrive(ml_full);
+            if (s.w == 2 || two || wg == 0) {
+                s_l[((uses & 1) * 4 + wg * 2 + half) * 128 + t] = l;
+                if (two && wg == 1 && half == 0) s_m1[(uses & 1) * 128 + t] = m;
+                mbar_arrive(ml_full + wg);
             }
             if (s.w == 2 || wg == 0) {
+                if (!(ok = warp_wait(ml_full + wg, uses & 1, abort_flag, a.err))) break;
+                l += s_l[((uses & 1) * 4 + wg * 2 + (half ^ 1)) * 128 + t];
                 if (!(ok = warp_wait(o_full + wg, uses & 1, abort_flag, a.err))) break;
+                float f0 = 1.f, f1 = 0.f;
                 if (two) {
-                    if (!(ok = warp_wait(ml_full, joins & 1, abort_flag, a.err))) break;
+                    if (!(ok = warp_wait(ml_full + 1, uses1 & 1, abort_flag, a.err))) break;
                     if (!(ok = warp_wait(o_full + 1, uses1 & 1, abort_flag, a.err))) break;
-                    const float2 x = s_ml[(joins & 1) * 128 + t];
-                    const float mn = fmaxf(m, x.x);
+                    const float* l1 = s_l + ((uses1 & 1) * 4 + 2) * 128 + t;
+                    const float m1 = s_m1[(uses1 & 1) * 128 + t], mn = fmaxf(m, m1);
                     f0 = m == mn ? 1.f : ex2(m - mn);
-                    f1 = x.x == mn ? 1.f : ex2(x.x - mn);
+                    f1 = m1 == mn ? 1.f : ex2(m1 - mn);
                     m = mn;
-                    l = l * f0 + x.y * f1;
+                    l = l * f0 + (l1[0] + l1[128]) * f1;
                 }
                 tc_fence_after();
                 const bool bad = s_bad[seg & 3] == seg + 1;
@@ -559,47 +573,50 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int64_t row = s.r + mytok;
                 const int prow = (s.w == 2 ? wg * 128 : 0) + t;
                 float* part = paged_slot(a, blockIdx.x, slot);
-                if (valid && !whole) {
-                    part[prow] = m;
-                    part[a.slot_rows + prow] = l;
-                } else if (valid && a.lse) {
-                    a.lse[row * a.H + head] = (m + log2f(l)) * 0.693147180559945309f;
+                if (valid && half == 0) {
+                    if (!whole) {
+                        part[prow] = m;
+                        part[a.slot_rows + prow] = l;
+                    } else if (a.lse) {
+                        a.lse[row * a.H + head] = (m + log2f(l)) * 0.693147180559945309f;
+                    }
                 }
                 const float inv = whole ? 1.f / l : 1.f;
+                const int c0 = D / 2 * half;
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tmem_ld32(o_col + c, o);
+                for (int c = 0; c < D / 2; c += 16) {
+                    float o[16];
+                    tmem_ld16(o_col + c, o);
                     if (two) {
-                        float o1[32];
-                        tmem_ld32(o_col1 + c, o1);
-                        tmem_wait_ld32(o);
-                        tmem_wait_ld32(o1);
+                        float o1[16];
+                        tmem_ld16(o_col1 + c, o1);
+                        tmem_wait_ld16(o);
+                        tmem_wait_ld16(o1);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + o1[j] * f1;
+                        for (int j = 0; j < 16; ++j) o[j] = o[j] * f0 + o1[j] * f1;
                     } else {
-                        tmem_wait_ld32(o);
+                        tmem_wait_ld16(o);
                     }
-                    if (c + 32 == D) {
+                    if (c + 16 == D / 2) {
                         tc_fence_before();
                         mbar_arrive(o_free + wg);
                         if (two) mbar_arrive(o_free + 1);
                     }
                     if (valid && whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.o + (row * a.o_rs + (int64_t)head * D + c) * 2);
+                        uint4* dst = reinterpret_cast<uint4*>(a.o + (row * a.o_rs + (int64_t)head * D + c0 + c) * 2);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
+                        for (int j = 0; j < 16; j += 8)
                             dst[j / 8] = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
                                                     pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
                     } else if (valid) {
-                        float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows + (int64_t)prow * D + c);
+                        float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows + (int64_t)prow * D + c0 + c);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 16; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                     __syncwarp();
                 }
                 if (bad && valid) {  // onto what this thread has just written
-                    for (int c = 0; c < D; ++c) {
+                    for (int c = c0; c < c0 + D / 2; ++c) {
                         const float x = paged_nonfinite<kKT>(a, s, pos, c);
                         if (x == 0.f) continue;
                         __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(a.o) + row * a.o_rs + (int64_t)head * D + c;
@@ -610,7 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             uses1 += s.w == 2 || two;
             uses = wg ? uses1 : uses + 1;
-            joins += two;
             base += 2 * T;
             __syncwarp();
             if (lane == 0) mbar_arrive(seg_empty + (seg & 1));
@@ -682,8 +698,8 @@ cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int rows = a.page < kKT ? a.page : kKT;
     if (!paged_kv_map(&tm.k, a.k, a, rows) || !paged_kv_map(&tm.v, a.v, a, rows)) return cudaErrorInvalidValue;
-    if (a.d == 64) return launch<64, 12>(tm, a, grid, st);
+    if (a.d == 64) return launch<64, 11>(tm, a, grid, st);
     if (a.d == 96) return launch<96, 7>(tm, a, grid, st);
-    if (a.d == 128) return launch<128, 5>(tm, a, grid, st);
+    if (a.d == 128) return launch<128, 4>(tm, a, grid, st);
     return cudaErrorInvalidValue;
 }

@@ -6,7 +6,7 @@
 // group).  An item's keys are cut into tiles of KT; those no row can see (past the
 // last token, or behind the window and past the first `sinks` tokens) are left out.
 // An item costs its key tiles times its M tiles.  All items of the call, in the
-// order (sequence, row tile, head), form one line of that cost, and each CTA takes an
+// order (sequence, head, row tile), form one line of that cost, and each CTA takes an
 // equal stretch of it, whatever the mix of lengths: the lengths are on the device
 // only, so each CTA finds its own stretch from ctx_len and row0 (two block-wide
 // scans, about 2 us).  An item inside one stretch is finished by its CTA; one that
@@ -126,9 +126,11 @@ struct PagedSeg {
 };
 
 struct PagedPlanSmem {
-    int sq[kPagedMaxSeqs + 1];  // row tiles before each sequence
+    int64_t cp[kPagedMaxSeqs + 1];  // one head's cost before each sequence
+    int64_t tp[1024 + 1];           // one head's cost before each thread's run of row tiles
+    int sq[kPagedMaxSeqs + 1];      // row tiles before each sequence
     int64_t warp[32];
-    PagedSeg s;                 // where the CTA's stretch begins, as one thread finds it
+    PagedSeg s;                     // where the CTA's stretch begins, as one thread finds it
     int qt, off;
 };
 
@@ -180,20 +182,29 @@ struct PagedPlan {
         s.r = q.r;
     }
 
-    // The CTA's stretch of the line, given that the one-head cost `p` lies before the
-    // current item (the item that holds x / Hkv).
-    __device__ __forceinline__ void place(const PagedArgs& a, int64_t p) {
-        const int c = item(a);
-        const int64_t rem = x - p * a.Hkv;
-        s.head = (int)paged_div(rem, c);
-        off = (int)(rem - (int64_t)s.head * c);
-    }
     __device__ __forceinline__ void share(const PagedArgs& a, int64_t one_head, int min_cost) {
         const int64_t total = one_head * a.Hkv;
         int64_t len = paged_div(total + gridDim.x - 1, gridDim.x);
         len = len < min_cost ? min_cost : len;
         x = len * blockIdx.x;
         x_end = x + len < total ? x + len : total;
+    }
+    // The head that holds x, of the current sequence (one head of it costs `c`, `before`
+    // lies ahead of it); returns how far x is into that head's row tiles.
+    __device__ __forceinline__ int64_t head_of(const PagedArgs& a, int64_t before, int64_t c) {
+        const int64_t rem = x - before * a.Hkv;
+        s.head = (int)paged_div(rem, c);
+        return rem - s.head * c;
+    }
+    // The row tile that holds cost `y`, of those from the current one (after `p`).
+    __device__ __forceinline__ void tile_of(const PagedArgs& a, int64_t p, int64_t y) {
+        int c = item(a);
+        while (p + c <= y) {
+            p += c;
+            ++qt;
+            c = item(a);
+        }
+        off = (int)(y - p);
     }
 
     // All threads of the block; `sm` may be reused after the call (it ends with a barrier).
@@ -216,20 +227,13 @@ struct PagedPlan {
             int64_t total;
             const int64_t incl = paged_scan<THREADS>(cost, sm.warp, total);
             share(a, total, min_cost);
-            if (x < x_end) {
-                const int64_t y = paged_div(x, a.Hkv);
-                int64_t p = incl - cost;
-                if (p <= y && y < incl) {  // one thread's sequence
-                    qt = 0;
-                    for (int c = item(a); p + c <= y; c = item(a)) {
-                        p += c;
-                        ++qt;
-                    }
-                    place(a, p);
-                    sm.s = s;
-                    sm.qt = qt;
-                    sm.off = off;
-                }
+            if (x < x_end && (incl - cost) * a.Hkv <= x && x < incl * a.Hkv) {  // one thread's sequence
+                const int64_t y = head_of(a, incl - cost, cost);
+                qt = 0;
+                tile_of(a, 0, y);
+                sm.s = s;
+                sm.qt = qt;
+                sm.off = off;
             }
         } else {
             // row tiles before each sequence
@@ -245,8 +249,8 @@ struct PagedPlan {
             }
             if (tid == 0) sm.sq[0] = 0;
             __syncthreads();
-            // cost of each thread's run of row tiles
-            const int per = (base + THREADS - 1) / THREADS;
+            // cost before each thread's run of row tiles, and before each sequence
+            const int per = max(1, (base + THREADS - 1) / THREADS);
             const int q0 = min(base, tid * per), q1 = min(base, q0 + per);
             int64_t cost = 0, total;
             if (q0 < q1) {
@@ -257,21 +261,46 @@ struct PagedPlan {
                 }
             }
             const int64_t incl = paged_scan<THREADS>(cost, sm.warp, total);
-            share(a, total, min_cost);
-            if (x < x_end) {
-                const int64_t y = paged_div(x, a.Hkv);
-                int64_t p = incl - cost;
-                if (p <= y && y < incl) {  // one thread's run
-                    find(a, sm, q0);
-                    for (int c = item(a); p + c <= y; c = item(a)) {
-                        p += c;
+            sm.tp[tid] = incl - cost;
+            __syncthreads();
+            for (int i = tid; i <= a.nseq; i += THREADS) {
+                const int q = sm.sq[i], run = q / per;
+                int64_t p = q < base ? sm.tp[run] : total;
+                if (q < base) {
+                    find(a, sm, run * per);
+                    for (int j = run * per; j < q; ++j) {
+                        p += item(a);
                         step(a);
                     }
-                    place(a, p);
-                    sm.s = s;
-                    sm.qt = qt;
-                    sm.off = off;
                 }
+                sm.cp[i] = p;
+            }
+            __syncthreads();
+            share(a, total, min_cost);
+            if (x < x_end && tid == 0) {
+                int lo = 0, hi = a.nseq;  // the last sequence with cp * Hkv <= x: it has tiles
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (sm.cp[mid] * a.Hkv <= x) lo = mid; else hi = mid;
+                }
+                load(a, lo);
+                const int64_t y = sm.cp[lo] + head_of(a, sm.cp[lo], sm.cp[lo + 1] - sm.cp[lo]);
+                int r0 = 0, r1 = THREADS;  // the last run that begins at or before y
+                while (r1 - r0 > 1) {
+                    const int mid = (r0 + r1) / 2;
+                    if (mid * per < base && sm.tp[mid] <= y) r0 = mid; else r1 = mid;
+                }
+                // from there, or from the sequence's first row tile
+                qt = r0 * per - sm.sq[lo];
+                int64_t p = sm.tp[r0];
+                if (qt < 0) {
+                    qt = 0;
+                    p = sm.cp[lo];
+                }
+                tile_of(a, p, y);
+                sm.s = s;
+                sm.qt = qt;
+                sm.off = off;
             }
         }
         __syncthreads();
@@ -317,9 +346,15 @@ struct PagedPlan {
             out.tb = s.w == 2 ? end >> 1 : end;
             x += end - off;
             off = 0;
-            if (++s.head == a.Hkv) {
-                s.head = 0;
-                if (x < x_end) step(a);
+            if (++qt * (int64_t)a.tpt >= s.n) {
+                qt = 0;
+                if (++s.head == a.Hkv) {
+                    s.head = 0;
+                    if (x < x_end) {
+                        do load(a, s.seq + 1);
+                        while (s.n == 0);
+                    }
+                }
             }
             if (out.tb > out.ta) return true;
         }

@@ -10,15 +10,17 @@
 // accumulator need not be read back.  l sums the unrounded P; P is rounded to bf16 for
 // the second product (2^-8 of a weight at most, below the rounding of O itself).
 //
-// One persistent CTA per SM, 10 warps: two softmax warpgroups (one row per thread), a
-// TMA warp, an MMA warp.  Two streams s = 0, 1, each with its own S and O in tensor
-// memory (S 2 x 128 columns, P over S, O 2 x d columns), keep the tensor pipe busy with
-// one stream's products while the other's softmax runs:
+// One persistent CTA per SM, 12 warps: two groups of four softmax warps (a row per
+// thread), the MMA warp, three TMA warps.  Two streams s = 0, 1, one per softmax group,
+// each with two S buffers (64 keys each) and its own O in tensor memory:
 //   two M tiles (more than 128 rows): stream s is M tile s, both over the same key tile;
 //   one M tile: stream s takes every second key tile, joined at the item's end.
-// Keys and values arrive in 128-key tiles through one ring of shared-memory stages (K
-// and V in turn), one TMA box per page (or 128 rows of it) and 32 channels, 64-byte
-// swizzle.
+// S of a stream's next key tile is already there when its softmax ends a tile, so neither
+// the exponentials nor the tensor pipe wait for the other's latency.  (With one S buffer
+// of 128 keys per stream the chain softmax -> P V -> Q K^T -> softmax took 4400 cycles a
+// pair of tiles, of which the exponential unit and the tensor pipe were each busy 2100.)
+// Keys and values arrive in 64-key tiles through one ring of shared-memory stages, one
+// TMA box per page (or 64 rows of it) and 32 channels, 64-byte swizzle.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -35,10 +37,10 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kKT = 128;       // keys per tile
-constexpr int kThreads = 640;  // softmax warps 0-15 (8 a stream), the MMA warp, three TMA warps
-constexpr int kMmaWarp = 16, kTmaWarp = 17, kTmaWarps = 3;
-constexpr int kMinCost = 4;    // key tiles x M tiles a CTA takes at least (two key tiles of two M tiles)
+constexpr int kKT = 64;  // keys per tile
+constexpr int kThreads = 384;  // softmax warps 0-7 (4 a stream), the MMA warp, three TMA warps
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kTmaWarps = 3;
+constexpr int kMinCost = 8;    // key tiles x M tiles a CTA takes at least
 
 struct alignas(64) PagedMaps {
     CUtensorMap q, k, v;
@@ -47,18 +49,19 @@ struct alignas(64) PagedMaps {
 template <int D, int ST>
 struct Lay {
     static constexpr int NCH = D / 32;         // 32-channel chunks
-    static constexpr int TILE = NCH * 8192;    // 128 rows of bf16
+    static constexpr int QTILE = NCH * 8192;   // 128 rows of bf16
+    static constexpr int TILE = NCH * 4096;    // 64 keys of bf16
     static constexpr int Q = 0;
-    static constexpr int KV = 2 * TILE;
+    static constexpr int KV = 2 * QTILE;
     static constexpr int BARS = KV + ST * TILE;
-    static constexpr int NBAR = 2 * ST + 7 * 2 + 3 + 16;
-    static constexpr int MX = BARS + ((NBAR * 8 + 15) / 16) * 16;  // [stream][half][128] maximum of a row's half
-    static constexpr int ML = MX + 4 * 128 * 4;                    // [2][stream][half][128] l at an item's end, then [2][128] m of stream 1
-    static constexpr int SEG = ML + 10 * 128 * 4;  // the segments under way, as the TMA warp found them
+    static constexpr int NBAR = 2 * ST + 2 * 4 + 6 * 2 + 3;
+    static constexpr int ML = BARS + ((NBAR * 8 + 15) / 16) * 16;  // [2][128] (m, l) of stream 1
+    static constexpr int SEG = ML + 2 * 128 * 8;  // the segments under way, as the TMA warp found them
     static constexpr int MISC = SEG + 2 * 64;
-    static constexpr int TOTAL = MISC + 64;
+    static constexpr int TOTAL = MISC + 32;
     static_assert(sizeof(PagedSeg) <= 64, "segment slots");
     static_assert(sizeof(PagedPlanSmem) <= (size_t)ST * TILE, "plan arrays over the stages");
+    static_assert(ST >= 8, "the first products of an item need four key tiles, and its first values");
     static_assert(TOTAL + 512 <= 232448, "shared memory of one CTA");
 };
 
@@ -77,7 +80,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// Exponential and packing that stay where they are written.
+// Arithmetic that stays where it is written.
+__device__ __forceinline__ float fma_here(float a, float b, float c) {
+    float d;
+    asm volatile("fma.rn.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ float ex2_here(float x) {
     float y;
     asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -91,28 +99,26 @@ __device__ __forceinline__ uint32_t pack_here(float lo, float hi) {
 // The lowest n bits (all for n >= 32, none for n <= 0).
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
 // -inf where `see` has no bit.
-template <int N>
 __device__ __forceinline__ void hide(float* v, uint32_t see) {
-    constexpr uint32_t kAll = N == 32 ? ~0u : (1u << N) - 1;
-    if (__all_sync(0xffffffffu, (see & kAll) == kAll)) return;
+    if (__all_sync(0xffffffffu, see == ~0u)) return;
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = (see >> j) & 1 ? v[j] : -INFINITY;
+    for (int j = 0; j < 32; ++j) v[j] = (see >> j) & 1 ? v[j] : -INFINITY;
 }
 
 // Zeros the values the matrix product must not see in a key tile that some row sees
 // only in part: keys from `end` (of the tile) on, whose slots hold anything, and values
 // that are not finite (returns whether there were any; paged_nonfinite puts them back
-// where they are seen).  256 threads, 16 bytes at a time in the order they lie.  With two
+// where they are seen).  128 threads, 16 bytes at a time in the order they lie.  With two
 // M tiles both streams clean the tile, each before its own product: what the later one
 // still writes is what the earlier one wrote.
 template <int NCH>
 __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
     bool found = false;
 #pragma unroll 4
-    for (int i = t; i < NCH * 512; i += 256) {
+    for (int i = t; i < NCH * 256; i += 128) {
         uint4* at = reinterpret_cast<uint4*>(sv) + i;
         uint4 x = *at;
-        if (((i & 511) >> 2) >= end) {  // four 16-byte units a key
+        if (((i & 255) >> 2) >= end) {  // four 16-byte units a key
             if (x.x | x.y | x.z | x.w) *at = make_uint4(0, 0, 0, 0);
             continue;
         }
@@ -130,59 +136,45 @@ __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
     return found;
 }
 
-// Half a key tile of one row: S (64 columns at s_col) -> P over its first 32 columns, the
-// running maximum m (log2 units; the whole row's, the other half's warp tells its own
-// through `mx_mine`/`mx_other`) and this half's sum l, and half of O (D/2 columns at
-// o_col) rescaled where the maximum moved.  PART: keys past `hi`, or up to `lo` and not
-// below `first` (from the first of the 64), are hidden.  Two code paths, because the test
-// alone costs the full tiles a third of their time once the compiler turns it into
-// selects.  False if the wait for the other half gave up.
+// One key tile of one row: S (64 columns, on their way into x and y) -> P over its first
+// 32 columns (at s_col), the running maximum m (log2 units) and sum l, and O (at o_col)
+// rescaled where the maximum moved, once the product before (`pv_done`) has left it.  n:
+// tiles of the item before this one.  PART: keys past `hi`, or up to `lo` and not below
+// `first` (from the tile's first key), are hidden.  Two code paths, because the test alone
+// costs the full tiles a third of their time once the compiler turns it into selects.
+// False if a wait gave up.
 template <int D, bool PART>
-__device__ __forceinline__ bool softmax_step(uint32_t s_col, uint32_t o_col, float c2, int hi, int lo, int first, bool valid,
-                                             bool have_o, float& m, float& l, float* mx_mine, volatile float* mx_other,
-                                             uint64_t* bar_mine, uint64_t* bar_other, uint32_t parity, int lane,
-                                             volatile int* abort, int32_t* err) {
-    // Two passes over S: the second read costs less than holding the scores.
-    uint32_t see[2] = {~0u, ~0u};
+__device__ __forceinline__ bool softmax_step(float* x, float* y, uint32_t s_col, uint32_t o_col, float c2, int hi, int lo,
+                                             int first, bool valid, int n, float& m, float& l, uint64_t* pv_done,
+                                             uint32_t parity, volatile int* abort, int32_t* err) {
+    tmem_wait_ld32(x);
+    tmem_wait_ld32(y);
     if (PART) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            see[c] = below(hi + 1 - 32 * c) & (~below(lo + 1 - 32 * c) | below(first - 32 * c));
+        hide(x, below(hi + 1) & (~below(lo + 1) | below(first)));
+        hide(y, below(hi - 31) & (~below(lo - 31) | below(first - 32)));
     }
-    float mx;
-    {
-        float x[32], y[32];
-        tmem_ld32(s_col, x);
-        tmem_ld32(s_col + 32, y);
-        tmem_wait_ld32(x);
-        tmem_wait_ld32(y);
-        if (PART) {
-            hide<32>(x, see[0]);
-            hide<32>(y, see[1]);
-        }
-        float m0 = x[0], m1 = y[0];
+    float m0 = x[0], m1 = x[1], m2 = y[0], m3 = y[1];
 #pragma unroll
-        for (int j = 1; j < 31; j += 2) {
-            m0 = max3(m0, x[j], x[j + 1]);
-            m1 = max3(m1, y[j], y[j + 1]);
-        }
-        mx = fmaxf(max3(m0, x[31], y[31]), m1);
+    for (int j = 2; j < 30; j += 4) {
+        m0 = max3(m0, x[j], x[j + 1]);
+        m1 = max3(m1, x[j + 2], x[j + 3]);
+        m2 = max3(m2, y[j], y[j + 1]);
+        m3 = max3(m3, y[j + 2], y[j + 3]);
     }
-    *mx_mine = mx;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_other);
-    if (!__all_sync(0xffffffffu, mbar_wait_idle(bar_mine, parity, abort, err))) return false;
-    mx = fmaxf(mx, *mx_other) * c2;
+    m0 = max3(m0, x[30], x[31]);
+    m2 = max3(m2, y[30], y[31]);
+    const float mx = max3(m0, m1, fmaxf(m2, m3)) * c2;
     const bool grow = valid && mx > m + 8.f;  // m = -inf: any finite maximum
     if (__any_sync(0xffffffffu, grow)) {
         const float mn = grow ? mx : m;
         const float f = m == mn ? 1.f : ex2(m - mn);  // 0 from m = -inf
         m = mn;
         l *= f;
-        if (have_o) {
-            // The stream's earlier P V are complete: s_full came after them.
+        if (n > 0) {
+            if (!warp_wait(pv_done, parity, abort, err)) return false;
+            tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < D / 2; c += 16) {
+            for (int c = 0; c < D; c += 16) {
                 float o[16];
                 tmem_ld16(o_col + c, o);
                 tmem_wait_ld16(o);
@@ -192,37 +184,50 @@ __device__ __forceinline__ bool softmax_step(uint32_t s_col, uint32_t o_col, flo
             }
         }
     }
-    const float mref = m == -INFINITY ? 0.f : m;
-    // Exponentials of chunk c while chunk c - 1 is summed and packed: written out in
-    // that order (the asm statements keep it), because the exponential unit takes a
-    // warp 8 cycles an instruction and a warp that waits for each result idles it.
-    float l0 = 0.f, l1 = 0.f;
-    float v[3][16];
-    tmem_ld16(s_col, v[0]);
+    const float mref = m == -INFINITY ? 0.f : -m;
+    // The exponential unit takes a warp 8 cycles an instruction, and a warp that waits for
+    // each result idles it: the other work is written out between the exponentials (the
+    // asm statements keep their order), the second half's scaling beside the first half's
+    // exponentials, the first half's sums and packing beside the second's.
+    float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+    uint32_t w[16];
 #pragma unroll
-    for (int c = 0; c <= 4; ++c) {
-        float *x = v[c % 3], *y = v[(c + 2) % 3];
-        uint32_t w[8];
-        if (c < 4) {
-            tmem_wait_ld16(x);
-            if (c < 3) tmem_ld16(s_col + 16 * (c + 1), v[(c + 1) % 3]);
-            if (PART) hide<16>(x, see[c / 2] >> (c % 2 * 16));
+    for (int j = 0; j < 8; ++j) x[j] = fma_here(x[j], c2, mref);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = fmaf(x[j], c2, -mref);
-        }
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            if (c < 4) x[j] = ex2_here(x[j]);
-            if (c > 0) {
-                l0 += y[j];
-                l1 += y[j + 1];
-            }
-            if (c < 4) x[j + 1] = ex2_here(x[j + 1]);
-            if (c > 0) w[j / 2] = pack_here(y[j], y[j + 1]);
-        }
-        if (c > 0) tmem_st8(s_col + 8 * (c - 1), w);  // over columns read before
+    for (int j = 0; j < 32; ++j) {
+        x[j] = ex2_here(x[j]);
+        if (j < 24) x[j + 8] = fma_here(x[j + 8], c2, mref);
+        else y[j - 24] = fma_here(y[j - 24], c2, mref);
     }
-    l += l0 + l1;
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        y[j] = ex2_here(y[j]);
+        if (j < 24) y[j + 8] = fma_here(y[j + 8], c2, mref);
+        l0 += x[j];
+        w[j / 2] = pack_here(x[j], x[j + 1]);
+        y[j + 1] = ex2_here(y[j + 1]);
+        if (j < 24) y[j + 9] = fma_here(y[j + 9], c2, mref);
+        l1 += x[j + 1];
+        y[j + 2] = ex2_here(y[j + 2]);
+        if (j < 24) y[j + 10] = fma_here(y[j + 10], c2, mref);
+        l2 += x[j + 2];
+        w[j / 2 + 1] = pack_here(x[j + 2], x[j + 3]);
+        y[j + 3] = ex2_here(y[j + 3]);
+        if (j < 24) y[j + 11] = fma_here(y[j + 11], c2, mref);
+        l3 += x[j + 3];
+    }
+    tmem_st16(s_col, w);
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        w[j / 2] = pack_here(y[j], y[j + 1]);
+        w[j / 2 + 1] = pack_here(y[j + 2], y[j + 3]);
+        l0 += y[j];
+        l1 += y[j + 1];
+        l2 += y[j + 2];
+        l3 += y[j + 3];
+    }
+    tmem_st16(s_col + 16, w);
+    l += (l0 + l1) + (l2 + l3);
     return true;
 }
 
@@ -236,11 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     char* sQ = smem + L::Q;
     char* sKV = smem + L::KV;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BARS);
-    uint64_t *kv_full = bars, *kv_empty = bars + ST, *s_full = bars + 2 * ST, *p_full = s_full + 2, *o_full = p_full + 2,
-             *o_free = o_full + 2, *seg_full = o_free + 2, *seg_empty = seg_full + 2, *ml_full = seg_empty + 2, *q_full = ml_full + 2,
-             *q_free = q_full + 1, *drain = q_free + 1, *mx_full = drain + 1;
-    float* s_mx = reinterpret_cast<float*>(smem + L::MX);
-    float *s_l = reinterpret_cast<float*>(smem + L::ML), *s_m1 = s_l + 8 * 128;
+    // s_full, p_full: [stream][S buffer]; the others with two: [stream] or [parity of the segment]
+    uint64_t *kv_full = bars, *kv_empty = bars + ST, *s_full = bars + 2 * ST, *p_full = s_full + 4, *pv_done = p_full + 4,
+             *o_full = pv_done + 2, *o_free = o_full + 2, *seg_full = o_free + 2, *seg_empty = seg_full + 2,
+             *q_full = seg_empty + 2, *q_free = q_full + 1, *ml_full = q_free + 1, *drain = ml_full + 1;
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::ML);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::MISC + 4);
     PagedSeg* s_seg[2] = {reinterpret_cast<PagedSeg*>(smem + L::SEG), reinterpret_cast<PagedSeg*>(smem + L::SEG + 64)};
@@ -252,18 +257,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             mbar_init(kv_full + i, 1);
             mbar_init(kv_empty + i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 256);
+            mbar_init(p_full + i, 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(pv_done + i, 1);
             mbar_init(o_full + i, 1);
-            mbar_init(o_free + i, 256);
-            mbar_init(ml_full + i, 256);
+            mbar_init(o_free + i, 128);
             mbar_init(seg_full + i, 1);
-            mbar_init(seg_empty + i, 16 + kTmaWarps);  // all but the warp that fills it
+            mbar_init(seg_empty + i, 8 + kTmaWarps);  // all but the warp that fills it
         }
         mbar_init(q_full, 1);
         mbar_init(q_free, 1);
-        for (int i = 0; i < 16; ++i) mbar_init(mx_full + i, 1);
+        mbar_init(ml_full, 128);
         mbar_init(drain, 1);
         fence_barrier_init();
         *abort_flag = 0;
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         const int pb = a.page < kKT ? a.page : kKT, nsub = kKT / pb;
         const int sub = b / NCH, ch = b % NCH;
         const uint32_t box = (uint32_t)pb * 64;
-        char* dst = sKV + ch * 8192 + sub * (int)box;
+        char* dst = sKV + ch * 4096 + sub * (int)box;
         int st = 0, ph = 1, n = 0;  // stage, its empty parity (the first round passes), segments begun
         bool ok = true;
         for (;; ++n) {
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             const int ta = slot->ta, tb = slot->tb;
             if (ta == tb) break;
-            const int end = slot->c + slot->t0 + slot->ntok, head = slot->head, seq = slot->seq;
+            const int end = slot->c + slot->t0 + slot->ntok, head = slot->head, seq = slot->seq, slot_w = slot->w;
             const PagedTiles tiles = slot->tiles;
             if (pw == 0) {
                 if (!(ok = warp_wait(q_free, (n & 1) ^ 1, abort_flag, a.err))) break;
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     mbar_expect_tx(q_full, slot->w * NCH * ((uint32_t)a.tok1 * a.G * 64));
                     for (int mt = 0; mt < slot->w; ++mt)
                         for (int c = 0; c < NCH; ++c)
-                            tma_load_3d(sQ + (mt * NCH + c) * 8192, &tm.q, 32 * c, head * a.G,
+                            tma_load_3d(sQ + mt * L::QTILE + c * 8192, &tm.q, 32 * c, head * a.G,
                                         slot->r + slot->t0 + mt * a.tok1, q_full);
                 }
                 __syncwarp();
@@ -327,28 +334,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) mbar_arrive(seg_empty + (n & 1));
             }
+            // The order of use: the first `ahead` key tiles, then each tile's values and the
+            // keys `ahead` tiles on.
+            const int ahead = slot_w == 2 ? 2 : 4;
             auto page_of = [&](int t) {
                 const int key = tiles.tile(t) * kKT + sub * pb;
                 return t < tb && sub < nsub && key < end ? paged_page(a, seq, key) : -1;
             };
-            int id = page_of(ta);
-            for (int t = ta; t < tb && ok; ++t) {
-                const int next_id = page_of(t + 1);
+            auto load = [&](int t, int id, const CUtensorMap* map) {
                 const int k0 = tiles.tile(t) * kKT, y = (k0 + sub * pb) & (a.page - 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (!(ok = warp_wait(kv_empty + st, ph, abort_flag, a.err))) break;
-                    if (pw == 0 && lane == 0)
-                        mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
-                    if (id >= 0) tma_load_4d(dst + st * L::TILE, kv ? &tm.v : &tm.k, 32 * ch, y, head, id, kv_full + st);
-                    __syncwarp();
-                    if (++st == ST) {
-                        st = 0;
-                        ph ^= 1;
-                    }
+                if (!warp_wait(kv_empty + st, ph, abort_flag, a.err)) return false;
+                if (pw == 0 && lane == 0) mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
+                if (id >= 0) tma_load_4d(dst + st * L::TILE, map, 32 * ch, y, head, id, kv_full + st);
+                __syncwarp();
+                if (++st == ST) {
+                    st = 0;
+                    ph ^= 1;
                 }
-                id = next_id;
+                return true;
+            };
+            int ids[4];  // pages of tiles t .. t + 3, of this lane's box
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ids[i] = page_of(ta + i);
+            ok = load(ta, ids[0], &tm.k);
+            for (int i = 1; i < ahead && ta + i < tb && ok; ++i)
+                ok = load(ta + i, i == 1 ? ids[1] : i == 2 ? ids[2] : ids[3], &tm.k);
+            for (int t = ta; t < tb && ok; ++t) {
+                const int next = page_of(t + 4);
+                if (!(ok = load(t, ids[0], &tm.v))) break;
+                if (t + ahead < tb) ok = load(t + ahead, ahead == 2 ? ids[2] : next, &tm.k);
+                ids[0] = ids[1];
+                ids[1] = ids[2];
+                ids[2] = ids[3];
+                ids[3] = next;
             }
+            if (!ok) break;
         }
         // Every copy has landed before the CTA's shared memory goes away: on the ordinary
         // way out the MMA warp waited for all of them.  Otherwise a stage may lack the first
@@ -363,40 +383,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             constexpr uint32_t IDESC_QK = idesc_bf16(128, kKT, 0), IDESC_PV = idesc_bf16(128, D, 1);
             const uint64_t dq = smem_desc(smem_u32(sQ), 16, 512, kLayoutSwizzle64B);
             const uint64_t dk = smem_desc(smem_u32(sKV), 16, 512, kLayoutSwizzle64B);
-            const uint64_t dv = smem_desc(smem_u32(sKV), 8192, 512, kLayoutSwizzle64B);
-            int seg = 0, st0 = 0, ph0 = 0;  // the segment's first stage
-            uint32_t steps[2] = {0, 0}, uses[2] = {0, 0};
+            const uint64_t dv = smem_desc(smem_u32(sKV), 4096, 512, kLayoutSwizzle64B);
+            int seg = 0, st = 0;
+            uint32_t ph = 0;                                         // the next stage in the order of use
+            uint32_t nqk[2] = {0, 0}, npv[2] = {0, 0}, uses[2] = {0, 0};  // products and segments of each stream so far
             bool ok = true;
-            // stage `k` places after (st0, ph0); k < 2 * ST
-            auto at = [&](int k, int& st, uint32_t& ph) {
-                st = st0 + k;
-                ph = ph0;
-                while (st >= ST) {
-                    st -= ST;
+            auto stage = [&]() -> bool {  // waits for it
+                return mbar_wait_idle(kv_full + st, ph, abort_flag, a.err);
+            };
+            auto next_stage = [&]() {  // frees it once the products issued so far are done
+                mma_commit(kv_empty + st);
+                if (++st == ST) {
+                    st = 0;
                     ph ^= 1;
                 }
             };
-            // S of stream s = Q tile `qt` x K in stage st
-            auto qk = [&](auto s, int qt, int st) {
+            // S of stream s (its next buffer) = Q tile `qt` x K in the current stage
+            auto qk = [&](auto s, int qt) {
+                const uint32_t b = nqk[s.value]++ & 1;
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    constexpr uint32_t u = 1;  // 16-byte units
-                    const uint32_t o = ((ks >> 1) * 8192 + (ks & 1) * 32) / 16 * u;
-                    mma_bf16(tmem + 128 * s.value, dq + qt * (L::TILE / 16) + o, dk + st * (L::TILE / 16) + o, IDESC_QK,
-                             ks > 0 ? 1u : 0u);
-                }
-                mma_commit(s_full + s.value);
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(tmem + 128 * s.value + 64 * b, dq + qt * (L::QTILE / 16) + ((ks >> 1) * 8192 + (ks & 1) * 32) / 16,
+                             dk + st * (L::TILE / 16) + ((ks >> 1) * 4096 + (ks & 1) * 32) / 16, IDESC_QK, ks > 0 ? 1u : 0u);
+                mma_commit(s_full + 2 * s.value + b);
             };
-            // O of stream s += P x V in stage st; waits for P, and for O before its first use
-            auto pv = [&](auto s, bool first, int st, uint32_t ph) -> bool {
-                if (!mbar_wait_idle(p_full + s.value, steps[s.value]++ & 1, abort_flag, a.err)) return false;
+            // O of stream s += P x V in the current stage; waits for P, and for O before its first use
+            auto pv = [&](auto s, bool first, bool last) -> bool {
+                const uint32_t n = npv[s.value]++, b = n & 1;
+                if (!mbar_wait_idle(p_full + 2 * s.value + b, (n >> 1) & 1, abort_flag, a.err)) return false;
                 if (first && !mbar_wait_idle(o_free + s.value, (uses[s.value]++ & 1) ^ 1, abort_flag, a.err)) return false;
-                if (!mbar_wait_idle(kv_full + st, ph, abort_flag, a.err)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kKT / 16; ++ks)
-                    mma_bf16_ts(tmem + 256 + D * s.value, tmem + 128 * s.value + (ks & 3) * 8 + (ks >> 2) * 64,
+                    mma_bf16_ts(tmem + 256 + D * s.value, tmem + 128 * s.value + 64 * b + ks * 8,
                                 dv + st * (L::TILE / 16) + ks * 64, IDESC_PV, (!first || ks > 0) ? 1u : 0u);
+                mma_commit(pv_done + s.value);
+                if (last) mma_commit(o_full + s.value);
                 return true;
             };
             const std::integral_constant<int, 0> s0{};
@@ -409,64 +431,58 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 if (T == 0) break;
                 if (!(ok = mbar_wait_idle(q_full, seg & 1, abort_flag, a.err))) break;
                 ++seg;
-                int st, kst;
-                uint32_t ph, kph;
-                // stages in order: K 0, V 0, K 1, V 1, ...
-                at(0, st, ph);
-                if (!(ok = mbar_wait_idle(kv_full + st, ph, abort_flag, a.err))) break;
                 if (two) {
-                    qk(s0, 0, st);
-                    qk(s1, 1, st);
-                    mma_commit(kv_empty + st);
-                    if (T == 1) mma_commit(q_free);
-                    for (int i = 0; i < T; ++i) {
-                        at(1, st, ph);
-                        at(2, kst, kph);
-                        const bool last = i + 1 == T;
-                        if (!(ok = pv(s0, i == 0, st, ph))) break;
-                        if (last) {
-                            mma_commit(o_full);
-                        } else {
-                            if (!(ok = mbar_wait_idle(kv_full + kst, kph, abort_flag, a.err))) break;
-                            qk(s0, 0, kst);
-                        }
-                        if (!(ok = pv(s1, i == 0, st, ph))) break;
-                        mma_commit(kv_empty + st);
-                        if (last) {
-                            mma_commit(o_full + 1);
-                        } else {
-                            qk(s1, 1, kst);
-                            mma_commit(kv_empty + kst);
-                            if (i + 2 == T) mma_commit(q_free);
-                        }
-                        at(2, st0, kph);
-                        ph0 = kph;
-                    }
-                } else {
-                    qk(s0, 0, st);
-                    mma_commit(kv_empty + st);
-                    if (T > 1) {
-                        at(2, st, ph);
-                        if (!(ok = mbar_wait_idle(kv_full + st, ph, abort_flag, a.err))) break;
-                        qk(s1, 0, st);
-                        mma_commit(kv_empty + st);
+                    for (int i = 0; i < 2 && i < T && (ok = stage()); ++i) {
+                        qk(s0, 0);
+                        qk(s1, 1);
+                        next_stage();
                     }
                     if (T <= 2) mma_commit(q_free);
-                    for (int i = 0; i < T; ++i) {
-                        at(1, st, ph);
-                        if (!(ok = i & 1 ? pv(s1, i == 1, st, ph) : pv(s0, i == 0, st, ph))) break;
-                        mma_commit(kv_empty + st);
+                    for (int i = 0; i < T && ok; ++i) {
+                        if (!(ok = stage())) break;
+                        const int vst = st;
+                        if (!(ok = pv(s0, i == 0, i + 1 == T))) break;
                         if (i + 2 < T) {
-                            at(4, kst, kph);
-                            if (!(ok = mbar_wait_idle(kv_full + kst, kph, abort_flag, a.err))) break;
-                            if (i & 1) qk(s1, 0, kst); else qk(s0, 0, kst);
-                            mma_commit(kv_empty + kst);
+                            // the keys two tiles on lie in the next stage
+                            const uint32_t vph = ph;
+                            if (++st == ST) {
+                                st = 0;
+                                ph ^= 1;
+                            }
+                            const int kst = st;
+                            const uint32_t kph = ph;
+                            if (!(ok = stage())) break;
+                            qk(s0, 0);
+                            st = vst;
+                            ph = vph;
+                            if (!(ok = pv(s1, i == 0, false))) break;
+                            mma_commit(kv_empty + vst);
+                            st = kst;
+                            ph = kph;
+                            qk(s1, 1);
+                            next_stage();
                             if (i + 3 == T) mma_commit(q_free);
                         } else {
-                            mma_commit(o_full + (i & 1));
+                            if (!(ok = pv(s1, i == 0, i + 1 == T))) break;
+                            next_stage();
                         }
-                        at(2, st0, kph);
-                        ph0 = kph;
+                    }
+                } else {
+                    for (int i = 0; i < 4 && i < T && (ok = stage()); ++i) {
+                        if (i & 1) qk(s1, 0); else qk(s0, 0);
+                        next_stage();
+                    }
+                    if (T <= 4) mma_commit(q_free);
+                    for (int i = 0; i < T && ok; ++i) {
+                        if (!(ok = stage())) break;
+                        if (!(ok = i & 1 ? pv(s1, i == 1, i + 2 >= T) : pv(s0, i == 0, i + 2 >= T))) break;
+                        next_stage();
+                        if (i + 4 < T) {
+                            if (!(ok = stage())) break;
+                            if (i & 1) qk(s1, 0); else qk(s0, 0);
+                            next_stage();
+                            if (i + 5 == T) mma_commit(q_free);
+                        }
                     }
                 }
                 if (!ok) break;
@@ -479,60 +495,69 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue
-        // Warp: stream warp / 8, columns (of S and of O) of half (warp / 4) % 2, rows of
-        // quarter warp % 4.  Two warps a row, because one warp per scheduler and stream left
-        // the exponential unit half idle (2600 cycles a tile against 1060 at its rate).
-        const int wg = warp / 8, half = (warp / 4) % 2, t = threadIdx.x % 128;  // t: TMEM lane = row of the M tile
+        const int wg = warp / 4, t = threadIdx.x % 128;  // stream; TMEM lane = row of the M tile
         const uint32_t lane_addr = (uint32_t)((warp % 4) * 32) << 16;
-        const uint32_t s_col = tmem + 128 * wg + 64 * half + lane_addr, o_col1 = tmem + 256 + D + D / 2 * half + lane_addr,
-                       o_col = wg ? o_col1 : o_col1 - D;
-        float* mx_mine = s_mx + (wg * 2 + half) * 128 + t;
-        float* mx_other = s_mx + (wg * 2 + (half ^ 1)) * 128 + t;
+        const uint32_t s_col = tmem + 128 * wg + lane_addr, o_col1 = tmem + 256 + D + lane_addr, o_col = wg ? o_col1 : o_col1 - D;
         const float c2 = a.scale_log2;
         const int tok = t / a.G, g = t - tok * a.G;
-        int base = 0, seg = 0, steps = 0, uses = 0, uses1 = 0;  // uses: of this stream, and of stream 1, as in the MMA warp
+        int base = 0, seg = 0, joins = 0, uses = 0, uses1 = 0;  // uses: of this stream, and of stream 1, as in the MMA warp
+        uint32_t steps = 0;                                     // key tiles of this stream so far
         if (threadIdx.x == 0) a.hdr[blockIdx.x].kind = 0;
         bool ok = true;
         while (ok && (ok = warp_wait(seg_full + (seg & 1), (seg >> 1) & 1, abort_flag, a.err))) {
-            const PagedSeg& s = *s_seg[seg & 1];
+            const PagedSeg s = *s_seg[seg & 1];  // in registers: the loop below must not wait for loads
             const int T = s.tb - s.ta;
             if (T == 0) break;
+            const int ahead = s.w == 2 ? 2 : 4;
             const int mytok = s.t0 + (s.w == 2 ? wg * a.tok1 : 0) + tok;  // this row's token
             const bool valid = tok < a.tok1 && mytok < s.t0 + s.ntok;
             const int pos = s.c + mytok;
             const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1;
             const int nsteps = s.w == 2 ? T : (T + 1 - wg) / 2;
             float m = -INFINITY, l = 0.f;
-            for (int n = 0; n < nsteps && ok; ++n, ++steps) {
-                const int i = s.w == 2 ? n : 2 * n + wg;
-                const int k0 = s.tiles.tile(s.ta + i) * kKT;
-                const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
-                if (!(ok = warp_wait(s_full + wg, steps & 1, abort_flag, a.err))) break;
+            // paged_all_seen of a tile in three comparisons
+            const int full_hi = p0 - (kKT - 1), full_lo = a.window > 0 ? p1 - a.window : -1, full_first = a.sinks - kKT;
+            int tile = s.ta + (s.w == 2 ? 0 : wg);
+            float x[32], y[32];
+            auto scores = [&](uint32_t step) -> bool {  // waits for the stream's S of `step` and begins to load it
+                const uint32_t b = step & 1;
+                if (!warp_wait(s_full + 2 * wg + b, (step >> 1) & 1, abort_flag, a.err)) return false;
                 tc_fence_after();
+                tmem_ld32(s_col + 64 * b, x);
+                tmem_ld32(s_col + 64 * b + 32, y);
+                return true;
+            };
+            if (nsteps > 0) ok = scores(steps);
+            for (int n = 0; n < nsteps && ok; ++n, ++steps, tile += s.w == 2 ? 1 : 2) {
+                const int k0 = (tile < s.tiles.ts ? tile : tile - s.tiles.ts + s.tiles.tlo) * kKT;
+                const bool part = k0 > full_hi || (k0 <= full_lo && k0 > full_first);
+                const uint32_t b = steps & 1;
                 if (part) {
-                    // Only once the scores are there: they come after the products that used
-                    // the stage before, so the parity cannot be that of an earlier round.
-                    const int k = base + 2 * i + 1, st = k % ST;
+                    // The tile's values, in the order the TMA warps load.  Only once the scores are
+                    // there: their product was issued when every load up to `ahead` tiles back had
+                    // arrived, so the parity cannot be that of the stage's earlier round.
+                    const int i = tile - s.ta, k = base + min(T, ahead) + i + min(i, max(T - ahead, 0)), st = k % ST;
                     if (!(ok = warp_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
-                    if (clean_values<NCH>(sKV + st * L::TILE, threadIdx.x % 256, p1 + 1 - k0)) {
+                    if (clean_values<NCH>(sKV + st * L::TILE, t, p1 + 1 - k0)) {
                         s_bad[seg & 3] = seg + 1;
                         __threadfence_block();
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
+                    ok = softmax_step<D, true>(x, y, s_col + 64 * b, o_col, c2, pos - k0, a.window > 0 ? pos - a.window - k0 : -1,
+                                               a.sinks - k0, valid, n, m, l, pv_done + wg, (steps + 1) & 1, abort_flag, a.err);
+                } else {
+                    ok = softmax_step<D, false>(x, y, s_col + 64 * b, o_col, c2, 0, 0, 0, valid, n, m, l, pv_done + wg,
+                                                (steps + 1) & 1, abort_flag, a.err);
                 }
-                const int kh = k0 + 64 * half;
-                if (part)
-                    ok = softmax_step<D, true>(s_col, o_col, c2, pos - kh, a.window > 0 ? pos - a.window - kh : -1,
-                                               a.sinks - kh, valid, n > 0, m, l, mx_mine, mx_other, mx_full + warp,
-                                               mx_full + (warp ^ 4), steps & 1, lane, abort_flag, a.err);
-                else
-                    ok = softmax_step<D, false>(s_col, o_col, c2, 0, 0, 0, valid, n > 0, m, l, mx_mine, mx_other,
-                                                mx_full + warp, mx_full + (warp ^ 4), steps & 1, lane, abort_flag, a.err);
                 if (!ok) break;
+                // the next scores are on their way while P is
+                const bool more = n + 1 == nsteps || scores(steps + 1);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(p_full + wg);
+                mbar_arrive(p_full + 2 * wg + b);
+                ok = more;
+                if (!ok) break;
             }
             if (!ok) break;
             // -------------------------------------------------------- the item's end
@@ -547,25 +572,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 a.hdr[blockIdx.x] = h;
             }
             const bool two = s.w == 1 && T > 1;  // both streams hold a part of the one M tile
-            if (s.w == 2 || two || wg == 0) {
-                s_l[((uses & 1) * 4 + wg * 2 + half) * 128 + t] = l;
-                if (two && wg == 1 && half == 0) s_m1[(uses & 1) * 128 + t] = m;
-                mbar_arrive(ml_full + wg);
+            if (two && wg == 1) {
+                s_ml[(joins & 1) * 128 + t] = make_float2(m, l);
+                mbar_arrive(ml_full);
             }
             if (s.w == 2 || wg == 0) {
-                if (!(ok = warp_wait(ml_full + wg, uses & 1, abort_flag, a.err))) break;
-                l += s_l[((uses & 1) * 4 + wg * 2 + (half ^ 1)) * 128 + t];
-                if (!(ok = warp_wait(o_full + wg, uses & 1, abort_flag, a.err))) break;
                 float f0 = 1.f, f1 = 0.f;
+                if (!(ok = warp_wait(o_full + wg, uses & 1, abort_flag, a.err))) break;
                 if (two) {
-                    if (!(ok = warp_wait(ml_full + 1, uses1 & 1, abort_flag, a.err))) break;
+                    if (!(ok = warp_wait(ml_full, joins & 1, abort_flag, a.err))) break;
                     if (!(ok = warp_wait(o_full + 1, uses1 & 1, abort_flag, a.err))) break;
-                    const float* l1 = s_l + ((uses1 & 1) * 4 + 2) * 128 + t;
-                    const float m1 = s_m1[(uses1 & 1) * 128 + t], mn = fmaxf(m, m1);
+                    const float2 x = s_ml[(joins & 1) * 128 + t];
+                    const float mn = fmaxf(m, x.x);
                     f0 = m == mn ? 1.f : ex2(m - mn);
-                    f1 = m1 == mn ? 1.f : ex2(m1 - mn);
+                    f1 = x.x == mn ? 1.f : ex2(x.x - mn);
                     m = mn;
-                    l = l * f0 + (l1[0] + l1[128]) * f1;
+                    l = l * f0 + x.y * f1;
                 }
                 tc_fence_after();
                 const bool bad = s_bad[seg & 3] == seg + 1;
@@ -573,50 +595,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const int64_t row = s.r + mytok;
                 const int prow = (s.w == 2 ? wg * 128 : 0) + t;
                 float* part = paged_slot(a, blockIdx.x, slot);
-                if (valid && half == 0) {
-                    if (!whole) {
-                        part[prow] = m;
-                        part[a.slot_rows + prow] = l;
-                    } else if (a.lse) {
-                        a.lse[row * a.H + head] = (m + log2f(l)) * 0.693147180559945309f;
-                    }
+                if (valid && !whole) {
+                    part[prow] = m;
+                    part[a.slot_rows + prow] = l;
+                } else if (valid && a.lse) {
+                    a.lse[row * a.H + head] = (m + log2f(l)) * 0.693147180559945309f;
                 }
                 const float inv = whole ? 1.f / l : 1.f;
-                const int c0 = D / 2 * half;
 #pragma unroll
-                for (int c = 0; c < D / 2; c += 16) {
-                    float o[16];
-                    tmem_ld16(o_col + c, o);
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(o_col + c, o);
                     if (two) {
-                        float o1[16];
-                        tmem_ld16(o_col1 + c, o1);
-                        tmem_wait_ld16(o);
-                        tmem_wait_ld16(o1);
+                        float o1[32];
+                        tmem_ld32(o_col1 + c, o1);
+                        tmem_wait_ld32(o);
+                        tmem_wait_ld32(o1);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = o[j] * f0 + o1[j] * f1;
+                        for (int j = 0; j < 32; ++j) o[j] = o[j] * f0 + o1[j] * f1;
                     } else {
-                        tmem_wait_ld16(o);
+                        tmem_wait_ld32(o);
                     }
-                    if (c + 16 == D / 2) {
+                    if (c + 32 == D) {
                         tc_fence_before();
                         mbar_arrive(o_free + wg);
                         if (two) mbar_arrive(o_free + 1);
                     }
                     if (valid && whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.o + (row * a.o_rs + (int64_t)head * D + c0 + c) * 2);
+                        uint4* dst = reinterpret_cast<uint4*>(a.o + (row * a.o_rs + (int64_t)head * D + c) * 2);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8)
+                        for (int j = 0; j < 32; j += 8)
                             dst[j / 8] = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
                                                     pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
                     } else if (valid) {
-                        float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows + (int64_t)prow * D + c0 + c);
+                        float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows + (int64_t)prow * D + c);
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                     }
                     __syncwarp();
                 }
                 if (bad && valid) {  // onto what this thread has just written
-                    for (int c = c0; c < c0 + D / 2; ++c) {
+                    for (int c = 0; c < D; ++c) {
                         const float x = paged_nonfinite<kKT>(a, s, pos, c);
                         if (x == 0.f) continue;
                         __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(a.o) + row * a.o_rs + (int64_t)head * D + c;
@@ -627,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             uses1 += s.w == 2 || two;
             uses = wg ? uses1 : uses + 1;
+            joins += two;
             base += 2 * T;
             __syncwarp();
             if (lane == 0) mbar_arrive(seg_empty + (seg & 1));
@@ -698,8 +718,8 @@ cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int rows = a.page < kKT ? a.page : kKT;
     if (!paged_kv_map(&tm.k, a.k, a, rows) || !paged_kv_map(&tm.v, a.v, a, rows)) return cudaErrorInvalidValue;
-    if (a.d == 64) return launch<64, 11>(tm, a, grid, st);
-    if (a.d == 96) return launch<96, 7>(tm, a, grid, st);
-    if (a.d == 128) return launch<128, 4>(tm, a, grid, st);
+    if (a.d == 64) return launch<64, 22>(tm, a, grid, st);
+    if (a.d == 96) return launch<96, 14>(tm, a, grid, st);
+    if (a.d == 128) return launch<128, 10>(tm, a, grid, st);
     return cudaErrorInvalidValue;
 }

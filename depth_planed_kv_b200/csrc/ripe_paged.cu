@@ -45,11 +45,11 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
                     if (ctx < 0 || ctx + (int64_t)(e - r0) > (int64_t)a.table_width * a.page) {
                         if (a.err) set_device_error(a.err, RIPE_DEVERR_CAPACITY);
                     } else {
-                        const int id = __ldg(a.table + seq * a.table_stride + pos / a.page);
+                        const int id = __ldg(a.table + seq * a.table_stride + (pos >> a.page_shift));
                         if (id < 0 || id >= a.npages) {
                             if (a.err) set_device_error(a.err, RIPE_DEVERR_PAGE);
                         } else {
-                            off = id * a.page_stride + (pos % a.page) * a.pos_stride;
+                            off = id * a.page_stride + (pos & (a.page - 1)) * a.pos_stride;
                         }
                     }
                 }
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                 const int r = i / nv, v = i - r * nv, key = k0 + r;
                 const bool on = key <= p1;  // later slots hold anything: read as zeros
                 const int64_t off = on ? (paged_page(a, s.seq, key) * a.page_stride + s.head * a.head_stride +
-                                          (key % a.page) * a.pos_stride) * ES + v * 16
+                                          (key & (a.page - 1)) * a.pos_stride) * ES + v * 16
                                        : 0;
                 cp_async16_zfill(dk + r * pitch + v * 16, a.k + off, on);
                 cp_async16_zfill(dk + tile + r * pitch + v * 16, a.v + off, on);

@@ -36,7 +36,7 @@ struct PagedArgs {
     int64_t page_stride, head_stride, pos_stride;  // elements
     const int32_t *table, *ctx, *row0;
     int64_t table_stride;
-    int table_width, nseq, nrows, H, Hkv, G, d, page, npages;
+    int table_width, nseq, nrows, H, Hkv, G, d, page, page_shift, npages;
     int window, sinks;  // window 0: none
     int max_ntok;       // longer sequences are skipped
     int tok1, tpt;      // tokens of one M tile and of one row tile (1 or 2 M tiles)
@@ -106,15 +106,22 @@ __device__ __forceinline__ bool paged_seen(const PagedArgs& a, int key, int pos)
     return key <= pos && (a.window <= 0 || key > pos - a.window || key < a.sinks);
 }
 
-// Page of key `key` of sequence `seq`: an id outside the pool is reported and read as
-// page 0 (that sequence's rows then mean nothing).
-__device__ __forceinline__ int paged_page(const PagedArgs& a, int seq, int key) {
-    int id = __ldg(a.table + seq * a.table_stride + key / a.page);
-    if (id < 0 || id >= a.npages) {
+// The table's entry for key `key` of sequence `seq`, to be passed through paged_checked
+// before use (apart, so that a load far ahead of its use waits for nothing).
+__device__ __forceinline__ int paged_entry(const PagedArgs& a, int seq, int key) {
+    return __ldg(a.table + seq * a.table_stride + (key >> a.page_shift));
+}
+// An id outside the pool is reported and read as page 0 (that sequence's rows then mean
+// nothing).
+__device__ __forceinline__ int paged_checked(const PagedArgs& a, int id) {
+    if ((unsigned)id >= (unsigned)a.npages) {
         set_device_error(a.err, RIPE_DEVERR_PAGE);
         id = 0;
     }
     return id;
+}
+__device__ __forceinline__ int paged_page(const PagedArgs& a, int seq, int key) {
+    return paged_checked(a, paged_entry(a, seq, key));
 }
 
 // A stretch of one item: key tiles [ta, tb) of its `nt`.
@@ -385,7 +392,7 @@ __device__ __noinline__ float paged_nonfinite(const PagedArgs& a, const PagedSeg
         for (int key = k0; key < k0 + KT && key <= pos; ++key) {
             if (!paged_seen(a, key, pos)) continue;
             const int64_t row = paged_page(a, s.seq, key) * a.page_stride + s.head * a.head_stride +
-                                (key % a.page) * a.pos_stride;
+                                (key & (a.page - 1)) * a.pos_stride;
             const float f = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.v)[row + c]);
             if (!isfinite(f)) sum += f;
         }

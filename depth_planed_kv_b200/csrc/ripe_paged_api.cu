@@ -124,6 +124,7 @@ void fill(PagedArgs& a, const ripe_pages_t* p, const ripe_paged_batch_t* b) {
     a.Hkv = p->Hkv;
     a.d = p->d;
     a.page = p->page;
+    for (a.page_shift = 4; (1 << a.page_shift) < p->page;) ++a.page_shift;
     a.npages = p->npages;
     a.err = b->err_dev;
 }

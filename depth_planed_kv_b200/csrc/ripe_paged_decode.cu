@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
             while (it_t < is.tb - is.ta) {
                 const int kb = is.tiles.tile(is.ta + it_t) * kKT + warp * 16, p0 = is.c + is.t0;
                 if (paged_any_seen(a, kb, 16, p0, p0 + is.ntok - 1)) {
-                    id = paged_page(a, is.seq, kb);
+                    id = paged_entry(a, is.seq, kb);
                     return;
                 }
                 ++it_t;
@@ -97,11 +97,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         if (!more) return;
         const int st = issued % NS;
         char* dst = st_base + st * 2 * L::BLK;
-        const int y = (is.tiles.tile(is.ta + it_t) * kKT + warp * 16) % a.page;
+        const int y = (is.tiles.tile(is.ta + it_t) * kKT + warp * 16) & (a.page - 1);
+        const int page = paged_checked(a, id);
         if (lane == 0) mbar_expect_tx(full + st, 2 * L::BLK);
         __syncwarp();
         if (lane < 2 * NCH)
-            tma_load_4d(dst + lane * 1024, lane < NCH ? &tm.k : &tm.v, 32 * (lane < NCH ? lane : lane - NCH), y, is.head, id,
+            tma_load_4d(dst + lane * 1024, lane < NCH ? &tm.k : &tm.v, 32 * (lane < NCH ? lane : lane - NCH), y, is.head, page,
                         full + st);
         ++issued;
         ++it_t;

@@ -337,15 +337,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             // The order of use: the first `ahead` key tiles, then each tile's values and the
             // keys `ahead` tiles on.
             const int ahead = slot_w == 2 ? 2 : 4;
-            auto page_of = [&](int t) {
-                const int key = tiles.tile(t) * kKT + sub * pb;
-                return t < tb && sub < nsub && key < end ? paged_page(a, seq, key) : -1;
-            };
+            auto on = [&](int t) { return t < tb && sub < nsub && tiles.tile(t) * kKT + sub * pb < end; };
+            auto entry = [&](int t) { return on(t) ? paged_entry(a, seq, tiles.tile(t) * kKT + sub * pb) : 0; };
             auto load = [&](int t, int id, const CUtensorMap* map) {
                 const int k0 = tiles.tile(t) * kKT, y = (k0 + sub * pb) & (a.page - 1);
                 if (!warp_wait(kv_empty + st, ph, abort_flag, a.err)) return false;
                 if (pw == 0 && lane == 0) mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
-                if (id >= 0) tma_load_4d(dst + st * L::TILE, map, 32 * ch, y, head, id, kv_full + st);
+                if (on(t)) tma_load_4d(dst + st * L::TILE, map, 32 * ch, y, head, paged_checked(a, id), kv_full + st);
                 __syncwarp();
                 if (++st == ST) {
                     st = 0;
@@ -353,14 +351,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 }
                 return true;
             };
-            int ids[4];  // pages of tiles t .. t + 3, of this lane's box
+            int ids[4];  // table entries of tiles t .. t + 3, for this lane's box
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ids[i] = page_of(ta + i);
+            for (int i = 0; i < 4; ++i) ids[i] = entry(ta + i);
             ok = load(ta, ids[0], &tm.k);
             for (int i = 1; i < ahead && ta + i < tb && ok; ++i)
                 ok = load(ta + i, i == 1 ? ids[1] : i == 2 ? ids[2] : ids[3], &tm.k);
             for (int t = ta; t < tb && ok; ++t) {
-                const int next = page_of(t + 4);
+                const int next = entry(t + 4);
                 if (!(ok = load(t, ids[0], &tm.v))) break;
                 if (t + ahead < tb) ok = load(t + ahead, ahead == 2 ? ids[2] : next, &tm.k);
                 ids[0] = ids[1];

@@ -290,16 +290,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 
     if (warp >= kTmaWarp) {
         // ------------------------------------------------------------ TMA producers
-        // A tile is nsub (pages, or 128 keys of one) x NCH boxes, dealt to the lanes of three
-        // warps: a lane's copy takes the warp about 64 cycles to issue, so with pages of 16
-        // keys one warp alone would hold a tile back for 4100 cycles (measured: 15 bytes per
-        // cycle and SM instead of the 23 that HBM gives).
-        const int pw = warp - kTmaWarp, b = lane * kTmaWarps + pw;
+        // A tile is nsub (pages, or 64 keys of one) x NCH boxes, one per lane.  A lane's copy
+        // takes its warp about 70 cycles to issue, and a load another 250 for its barriers, so
+        // three warps take the loads in turn: with pages of 16 keys one warp alone brings 11
+        // bytes per cycle (HBM gives an SM 23).  Each waits for its own stages only; that
+        // cannot be off by a round, because stages are freed in the order of use and a warp
+        // comes round every kTmaWarps < ST loads.
+        static_assert(kTmaWarps < ST, "see above");
+        const int pw = warp - kTmaWarp;
         const int pb = a.page < kKT ? a.page : kKT, nsub = kKT / pb;
-        const int sub = b / NCH, ch = b % NCH;
+        const int sub = lane / NCH, ch = lane % NCH;
         const uint32_t box = (uint32_t)pb * 64;
         char* dst = sKV + ch * 4096 + sub * (int)box;
-        int st = 0, ph = 1, n = 0;  // stage, its empty parity (the first round passes), segments begun
+        int st = 0, ph = 1, turn = 0, n = 0;  // stage, its empty parity (the first round passes), whose load, segments begun
         bool ok = true;
         for (;; ++n) {
             PagedSeg* slot = s_seg[n & 1];
@@ -341,10 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             auto entry = [&](int t) { return on(t) ? paged_entry(a, seq, tiles.tile(t) * kKT + sub * pb) : 0; };
             auto load = [&](int t, int id, const CUtensorMap* map) {
                 const int k0 = tiles.tile(t) * kKT, y = (k0 + sub * pb) & (a.page - 1);
-                if (!warp_wait(kv_empty + st, ph, abort_flag, a.err)) return false;
-                if (pw == 0 && lane == 0) mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
-                if (on(t)) tma_load_4d(dst + st * L::TILE, map, 32 * ch, y, head, paged_checked(a, id), kv_full + st);
-                __syncwarp();
+                if (turn == pw) {
+                    if (!warp_wait(kv_empty + st, ph, abort_flag, a.err)) return false;
+                    if (lane == 0) mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
+                    __syncwarp();
+                    if (on(t)) tma_load_4d(dst + st * L::TILE, map, 32 * ch, y, head, paged_checked(a, id), kv_full + st);
+                    __syncwarp();
+                }
+                if (++turn == kTmaWarps) turn = 0;
                 if (++st == ST) {
                     st = 0;
                     ph ^= 1;
@@ -369,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             if (!ok) break;
         }
         // Every copy has landed before the CTA's shared memory goes away: on the ordinary
-        // way out the MMA warp waited for all of them.  Otherwise a stage may lack the first
-        // warp's share of the bytes it expects, so give the copies time instead of waiting on it.
+        // way out the MMA warp waited for all of them.  Otherwise give those in flight time
+        // (a stage may be one that nobody loads any more).
         if (!ok || *abort_flag) {
             const long long t0 = clock64();
             while (clock64() - t0 < (1 << 20)) {}

@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -49,19 +50,6 @@ class ripe_branch_t(ctypes.Structure):
                 ("reserved", ctypes.c_int32 * 3)]
 
 
-class ripe_pages_t(ctypes.Structure):
-    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64), ("pos_stride", ctypes.c_int64), ("npages", ctypes.c_int32),
-                ("page", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("reserved", ctypes.c_int32 * 3)]
-
-
-class ripe_paged_batch_t(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("ctx_len", ctypes.c_void_p),
-                ("row0", ctypes.c_void_p), ("table_width", ctypes.c_int32), ("nseq", ctypes.c_int32),
-                ("nrows", ctypes.c_int32), ("max_ntok", ctypes.c_int32), ("err_dev", ctypes.c_void_p)]
-
-
 def _sig(name, args, res=ctypes.c_int):
     f = getattr(_lib, name)
     f.argtypes = args
@@ -90,9 +78,10 @@ _sig("ripe_cache_set_all_depths_kernel", [_P, _I])
 _sig("ripe_debug_stall_next_verify", [_P, ctypes.c_longlong])
 _sig("ripe_accept", [_I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P])
 _sig("ripe_sample", [_I, _I, _P, _I, ctypes.c_int64] + [_P] * 8)
-_sig("ripe_paged_append", [_P, _P, _P, _P, ctypes.c_int64, _P])
-_sig("ripe_paged_attn_workspace", [_P, _I, _I, ctypes.POINTER(ctypes.c_size_t)])
-_sig("ripe_paged_attn", [_P, _P, _I, _P, ctypes.c_int64, _I, _I, ctypes.c_float, _P, ctypes.c_int64, _P, _P,
+_B = ctypes.c_char_p  # ripe_pages_t and ripe_paged_batch_t, packed
+_sig("ripe_paged_append", [_B, _B, _P, _P, ctypes.c_int64, _P])
+_sig("ripe_paged_attn_workspace", [_B, _I, _I, ctypes.POINTER(ctypes.c_size_t)])
+_sig("ripe_paged_attn", [_B, _B, _I, _P, ctypes.c_int64, _I, _I, ctypes.c_float, _P, ctypes.c_int64, _P, _P,
                          ctypes.c_size_t, _P])
 _sig("ripe_cache_buffers", [_P] + [ctypes.POINTER(_P)] * 7)
 _sig("ripe_read_meta", [_P, _P, _P, _P, _P])
@@ -162,9 +151,15 @@ def ripe_accept(zp: torch.Tensor, zq: torch.Tensor, zf: Optional[torch.Tensor], 
     return tuple(out)
 
 
-def _on_device(t: torch.Tensor):
-    """The device of `t`, made current if it is not (the C entry points launch on the current device)."""
-    return torch.cuda.device(t.device)
+def _here(t: torch.Tensor) -> bool:
+    """The current device is that of `t` (the C entry points launch on the current device)."""
+    return t.get_device() == torch.cuda.current_device()
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream
 
 
 def ripe_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
@@ -175,46 +170,65 @@ def ripe_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[tor
     (int32): [nrows] each, or None.  Returns (token int32 [nrows], logprob float32
     [nrows])."""
     n, V = logits.shape
-    assert V == 1 or logits.stride(1) == 1, "a row's logits are adjacent"
+    assert logits.is_cuda and (V == 1 or logits.stride(1) == 1), "a row's logits are adjacent, in device memory"
+    if not _here(logits):
+        with torch.cuda.device(logits.device):
+            return ripe_sample(logits, u, temperature, top_k, top_p, min_p, stream)
+    dev = logits.device
+    ptrs = []
     for t, dt in ((u, torch.float32), (temperature, torch.float32), (top_k, torch.int32), (top_p, torch.float32),
                   (min_p, torch.float32)):
-        assert t is None or (t.dtype == dt and t.shape == (n,) and t.is_contiguous() and t.device == logits.device)
-    with _on_device(logits):
-        token = torch.empty(n, dtype=torch.int32, device=logits.device)
-        logprob = torch.empty(n, dtype=torch.float32, device=logits.device)
-        if stream is not None:
-            token.record_stream(stream)
-            logprob.record_stream(stream)
-        _check(_lib.ripe_sample(n, V, _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), _ptr(u), _ptr(temperature),
-                                _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(logprob), _stream(stream)),
-               "ripe_sample")
+        if t is None:
+            ptrs.append(None)
+        else:
+            assert t.dtype == dt and t.shape == (n,) and t.is_contiguous() and t.device == dev
+            ptrs.append(t.data_ptr())
+    token = torch.empty(n, dtype=torch.int32, device=dev)
+    logprob = torch.empty(n, dtype=torch.float32, device=dev)
+    if stream is not None:
+        token.record_stream(stream)
+        logprob.record_stream(stream)
+    _check(_lib.ripe_sample(n, V, logits.data_ptr(), _dtype_code(logits.dtype), logits.stride(0), *ptrs, token.data_ptr(),
+                            logprob.data_ptr(), _raw_stream(stream, logits)), "ripe_sample")
     return token, logprob
 
 
-def _pages(K: torch.Tensor, V: torch.Tensor) -> ripe_pages_t:
+# ripe_pages_t and ripe_paged_batch_t as the C library lays them out; packed bytes cost a
+# fraction of a ctypes structure, and a decode step's call counts in microseconds.
+_PAGES = struct.Struct("@PPqqq5i3i")
+_BATCH = struct.Struct("@PqPP4iP")
+
+
+def _pages(K: torch.Tensor, V: torch.Tensor) -> bytes:
     npages, Hkv, page, d = K.shape
-    assert V.shape == K.shape and V.dtype == K.dtype and V.device == K.device
-    ps, hs, js, one = K.stride()
-    assert one == 1 and V.stride() == (ps, hs, js, 1), "the channels of a page's rows are adjacent; K and V lie alike"
-    return ripe_pages_t(K.data_ptr(), V.data_ptr(), ps, hs, js, npages, page, Hkv, d, _dtype_code(K.dtype))
+    ps, hs, js, one = st = K.stride()
+    assert V.shape == K.shape and V.stride() == st and one == 1, "a row's channels are adjacent; K and V pages lie alike"
+    assert V.dtype == K.dtype and K.is_cuda and V.device == K.device
+    return _PAGES.pack(K.data_ptr(), V.data_ptr(), ps, hs, js, npages, page, Hkv, d, _dtype_code(K.dtype), 0, 0, 0)
 
 
-def _batch(table, ctx_len, row0, nrows, max_ntok, err, device) -> ripe_paged_batch_t:
-    nseq = ctx_len.numel()
-    for t in (table, ctx_len, row0) + (() if err is None else (err,)):
-        assert t.dtype == torch.int32 and t.device == device
-    assert table.dim() == 2 and table.shape[0] == nseq and row0.numel() == nseq + 1
-    assert ctx_len.is_contiguous() and row0.is_contiguous() and (table.shape[1] == 1 or table.stride(1) == 1)
-    return ripe_paged_batch_t(table.data_ptr(), table.stride(0), ctx_len.data_ptr(), row0.data_ptr(), table.shape[1], nseq,
-                              nrows, max_ntok, None if err is None else err.data_ptr())
+def _batch(table, ctx_len, row0, nrows, max_ntok, err, device) -> bytes:
+    nseq, width = table.shape
+    ts, one = table.stride()
+    i32 = torch.int32
+    assert ctx_len.shape == (nseq,) and row0.shape == (nseq + 1,)
+    assert table.dtype == i32 and ctx_len.dtype == i32 and row0.dtype == i32
+    assert table.device == device and ctx_len.device == device and row0.device == device
+    assert (one == 1 or width == 1) and ctx_len.is_contiguous() and row0.is_contiguous()
+    ep = 0
+    if err is not None:
+        assert err.dtype == i32 and err.device == device
+        ep = err.data_ptr()
+    return _BATCH.pack(table.data_ptr(), ts, ctx_len.data_ptr(), row0.data_ptr(), width, nseq, nrows, max_ntok, ep)
 
 
-def _rows(t: torch.Tensor, pages: torch.Tensor, heads: int) -> int:
-    """Checks a row array [nrows][heads][d] beside its pages; the elements between two rows."""
-    assert t.dim() == 3 and t.dtype == pages.dtype and t.device == pages.device
-    assert t.shape[1] == heads and t.shape[2] == pages.shape[3]
-    assert t.stride(2) == 1 and (heads == 1 or t.stride(1) == t.shape[2]), "a row's heads are adjacent"
-    return t.stride(0) if t.shape[0] > 1 else heads * t.shape[2]
+def _rows(t: torch.Tensor, shape, dtype, device) -> int:
+    """Checks a row array [nrows][heads][d]; the elements between two rows."""
+    assert t.shape == shape and t.dtype == dtype and t.device == device
+    n, heads, d = shape
+    rs, hs, one = t.stride()
+    assert one == 1 and (hs == d or heads == 1), "a row's heads are adjacent"
+    return rs if n > 1 else heads * d
 
 
 def ripe_paged_append(K: torch.Tensor, V: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor, table: torch.Tensor,
@@ -223,24 +237,38 @@ def ripe_paged_append(K: torch.Tensor, V: torch.Tensor, Kpages: torch.Tensor, Vp
     pages ([npages][Hkv][page][d], any strides): sequence i's rows row0[i]..row0[i+1]-1
     go behind its ctx_len[i] positions, through row i of the page table (int32
     [nseq][width]).  err: device int32, see ripe.h."""
-    assert K.shape == V.shape
-    stride = _rows(K, Kpages, Kpages.shape[1])
-    assert _rows(V, Vpages, Vpages.shape[1]) == stride, "K and V have one row stride"
     pages = _pages(Kpages, Vpages)
-    batch = _batch(table, ctx_len, row0, K.shape[0], max(1, K.shape[0]), err, K.device)
-    with _on_device(K):
-        _check(_lib.ripe_paged_append(ctypes.byref(pages), ctypes.byref(batch), K.data_ptr(), V.data_ptr(), stride,
-                                      _stream(stream)), "ripe_paged_append")
+    if not _here(K):
+        with torch.cuda.device(Kpages.device):
+            assert _here(K)
+            return ripe_paged_append(K, V, Kpages, Vpages, table, ctx_len, row0, err, stream)
+    dev, nrows, shape = Kpages.device, K.shape[0], K.shape
+    assert shape[1] == Kpages.shape[1] and shape[2] == Kpages.shape[3]
+    stride = _rows(K, shape, Kpages.dtype, dev)
+    assert _rows(V, shape, Kpages.dtype, dev) == stride, "K and V have one row stride"
+    batch = _batch(table, ctx_len, row0, nrows, max(1, nrows), err, dev)
+    _check(_lib.ripe_paged_append(pages, batch, K.data_ptr(), V.data_ptr(), stride, _raw_stream(stream, K)),
+           "ripe_paged_append")
+
+
+_work_bytes = {}  # by what the size depends on
+
+
+def _workspace(pages: bytes, Kpages: torch.Tensor, H: int, max_ntok: int) -> int:
+    shape = Kpages.shape
+    key = (Kpages.get_device(), H, shape[1], shape[3], Kpages.dtype, min(max_ntok, 17))
+    n = _work_bytes.get(key)
+    if n is None:
+        out = ctypes.c_size_t()
+        _check(_lib.ripe_paged_attn_workspace(pages, H, max_ntok, ctypes.byref(out)), "ripe_paged_attn_workspace")
+        n = _work_bytes[key] = out.value
+    return n
 
 
 def ripe_paged_attn_workspace(Kpages: torch.Tensor, H: int, max_ntok: int) -> int:
     """Bytes of device work space a ripe_paged_attn call needs."""
-    pages = _pages(Kpages, Kpages)
-    out = ctypes.c_size_t()
-    with _on_device(Kpages):
-        _check(_lib.ripe_paged_attn_workspace(ctypes.byref(pages), H, max_ntok, ctypes.byref(out)),
-               "ripe_paged_attn_workspace")
-    return out.value
+    with torch.cuda.device(Kpages.device):
+        return _workspace(_pages(Kpages, Kpages), Kpages, H, max_ntok)
 
 
 def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor, table: torch.Tensor, ctx_len: torch.Tensor,
@@ -251,28 +279,30 @@ def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor,
     [nrows][H][d]; lse: float32 [nrows][H]; the batch as for ripe_paged_append.
     max_ntok: host bound on one sequence's new tokens (None: nrows; a decode batch gives
     1).  work: device bytes (None: taken from torch's allocator for this call)."""
-    nrows, H, d = Q.shape
+    pages = _pages(Kpages, Vpages)
+    if not _here(Q):
+        with torch.cuda.device(Kpages.device):
+            assert _here(Q)
+            return ripe_paged_attn(Q, Kpages, Vpages, table, ctx_len, row0, O, lse, max_ntok, window, sinks, scale, work,
+                                   err, stream)
+    dev, dtype, shape = Kpages.device, Kpages.dtype, Q.shape
+    nrows, H, d = shape
+    assert d == Kpages.shape[3]
     if max_ntok is None:
         max_ntok = max(1, nrows)
-    qs = _rows(Q, Kpages, H)
-    os_ = _rows(O, Kpages, H)
-    assert O.shape == Q.shape
-    assert lse is None or (lse.dtype == torch.float32 and lse.shape == (nrows, H) and lse.is_contiguous()
-                           and lse.device == Q.device)
-    pages = _pages(Kpages, Vpages)
-    batch = _batch(table, ctx_len, row0, nrows, max_ntok, err, Q.device)
-    with _on_device(Q):
-        if work is None:
-            need = ctypes.c_size_t()
-            _check(_lib.ripe_paged_attn_workspace(ctypes.byref(pages), H, max_ntok, ctypes.byref(need)),
-                   "ripe_paged_attn_workspace")
-            work = torch.empty(need.value, dtype=torch.uint8, device=Q.device)
-            if stream is not None:
-                work.record_stream(stream)
-        assert work.device == Q.device and work.is_contiguous()
-        _check(_lib.ripe_paged_attn(ctypes.byref(pages), ctypes.byref(batch), H, Q.data_ptr(), qs, window, sinks, scale,
-                                    O.data_ptr(), os_, None if lse is None else lse.data_ptr(), work.data_ptr(),
-                                    work.numel() * work.element_size(), _stream(stream)), "ripe_paged_attn")
+    qs, os_ = _rows(Q, shape, dtype, dev), _rows(O, shape, dtype, dev)
+    lp = None
+    if lse is not None:
+        assert lse.dtype == torch.float32 and lse.shape == (nrows, H) and lse.is_contiguous() and lse.device == dev
+        lp = lse.data_ptr()
+    batch = _batch(table, ctx_len, row0, nrows, max_ntok, err, dev)
+    if work is None:
+        work = torch.empty(_workspace(pages, Kpages, H, max_ntok), dtype=torch.uint8, device=dev)
+        if stream is not None:
+            work.record_stream(stream)
+    assert work.device == dev and work.is_contiguous()
+    _check(_lib.ripe_paged_attn(pages, batch, H, Q.data_ptr(), qs, window, sinks, scale, O.data_ptr(), os_, lp,
+                                work.data_ptr(), work.nbytes, _raw_stream(stream, Q)), "ripe_paged_attn")
 
 
 def ripe_cache_bytes(layers, R, H, d, W, Tmax, max_seqs, kmax, dtype=torch.bfloat16) -> int:

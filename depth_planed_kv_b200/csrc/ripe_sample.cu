@@ -10,18 +10,22 @@
 // times the kept mass; its log probability is log(w_v / kept mass).
 //
 // A draw is a comparison of running sums with a border, so the sums must not depend on
-// rounding or on the order of additions: weights are computed in 64 bits and held as
-// integers of 2^-40 (a sum of 2^23 weights stays below 2^64), which add up exactly in
-// any order.  A row of V near-equal tokens has V borders 1/V apart; an error of 2^-41 of
-// the largest weight moves a border by at most 2^-41, where 32-bit sums would pick
-// another token in about one of 10^4 rows.
+// the order of additions, and a weight's error must be small against the borders of a
+// flat row, 1/V apart: weights are integers of 2^-46 of the largest (2^-40 above 2^17
+// tokens; a sum of V of them stays below 2^63), which add up exactly in any order, each
+// right to about 2^-32 of itself.  (With 32-bit exponentials and sums about one row in
+// 10^4 of 10^5 near-equal tokens would draw its neighbour.)
 //
 // One cluster of 1 to 8 CTAs per row; each CTA holds a contiguous slice of the row in
-// shared memory, so the logits are read from memory once.  The k-th token, and the one
-// where the mass passes p, are found by counting and summing into 1024 bins (linear in
-// z first, then linear in the ordered bit pattern inside the bin that holds the border)
-// until the bin holds one token or one value; CTAs exchange their bins through
-// distributed shared memory, one cluster barrier per level.
+// shared memory, so the logits are read from memory once.  The order's prefix is found
+// from 1024 bins, linear in z below the maximum, which the CTAs read from one another
+// through distributed shared memory:
+//   - few tokens down to the border's bin (most rows): they are gathered in the first
+//     CTA, ranked there by counting, and drawn from; the other CTAs are done;
+//   - top-p over a flatter row: the border's bin alone is gathered and ranked, then all
+//     CTAs sum what is kept;
+//   - else (a bin of many tokens): bins of the ordered bit pattern inside the border's
+//     bin, until it holds one token or one value.
 #include <math.h>
 
 #include "ripe_internal.cuh"
@@ -32,8 +36,9 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kMaxCluster = 8;
-constexpr double kOne = 1099511627776.0;  // 2^40: weight 1
-constexpr float kRange = 28.f;            // w < 2^-40 beyond this many units of T below the maximum
+constexpr int kList = kThreads / 2;  // tokens ranked in one CTA, two threads each
+constexpr float kRange = 28.f;  // the bins reach this many units of T below the maximum
+constexpr int kPow = 512;       // table of 2^(-i / 512)
 
 typedef unsigned long long u64;
 
@@ -45,6 +50,13 @@ struct SampleArgs {
     const int32_t* top_k;
     int32_t* token;
     float* logprob;
+    int bits;  // the largest weight is 2^bits
+};
+
+// A gathered token.
+struct alignas(16) Item {
+    unsigned key, idx;
+    u64 w;
 };
 
 // What a CTA tells the others of its cluster; two of them in turn, so that one cluster
@@ -57,12 +69,14 @@ struct Msg {
 
 struct Shared {
     unsigned cnt[2][kBins], lo[2][kBins], hi[2][kBins];  // bins: tokens, mass (low and high words)
+    Item list[kList];
+    unsigned pow2[kPow];  // 2^31 * 2^(-i / 512)
     Msg msg[2][kMaxCluster];
-    u64 wsum[kWarps];
+    u64 wsum[kWarps], scan[kWarps];
     float wmax[kWarps];
     int widx[kWarps];
-    u64 scan[kWarps];
-    u64 pick[5];
+    u64 pick[6];
+    unsigned listed, token;
 };
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -106,18 +120,41 @@ __device__ __forceinline__ unsigned key_of(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float logit_of(unsigned key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
 struct Row {
-    float m, scale0;  // maximum; bins per unit of z at the first level
-    double dm, it;    // maximum, 1 / T
-    // weight of logit x in units of 2^-40
+    float m, scale0;       // maximum; bins per unit of z at the first level
+    float c_hi, c_lo;      // log2(e) / T as a sum of two floats
+    double dm, it;         // maximum, 1 / T
+    int bits;
+    const unsigned* pow2;
+    // 2^bits * exp((x - m) / T), rounded.  t = (m - x) * c as p + e (the difference and the
+    // product each with their rounding error), t = k / 512 + r; 2^-t = 2^(-k / 512) (1 - q),
+    // q = 1 - 2^-r = a - a^2/2 + a^3/6 for a = r ln 2, |a| < 2^-10.5: the next term is below
+    // 2^-46, q is held to 2^-32 and the table to 2^-32.
     __device__ __forceinline__ u64 weight(float x) const {
-        if (x == m) return (u64)kOne;
-        const double y = ((double)x - dm) * it;
-        return y > -30.0 ? (u64)__double2ull_rn(exp(y) * kOne) : 0ull;
+        if (x == m) return 1ull << bits;
+        const float hi = m - x, bb = hi - m, lo = (m - (hi - bb)) - (x + bb);
+        const float p = hi * c_hi;
+        if (!(p < (float)(bits + 1))) return 0ull;  // also -inf
+        const float e = fmaf(hi, c_lo, fmaf(lo, c_hi, fmaf(hi, c_hi, -p)));
+        const float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the rounded integer in the low bits
+        const float y = fmaf(p, (float)kPow, kMagic);
+        const int k = __float_as_int(y) - __float_as_int(kMagic);
+        const float a = (fmaf(y - kMagic, -1.f / kPow, p) + e) * 0.693147180559945309f;
+        const float q = a * (1.f - a * (0.5f - a * 0.16666667f));
+        const int qi = __float_as_int(fmaf(q, 2147483648.f, kMagic)) - __float_as_int(kMagic);
+        const unsigned T = pow2[k & (kPow - 1)];
+        const u64 w = ((u64)T << 31) - (u64)((long long)qi * (long long)T);  // 2^62 * 2^-frac
+        const int sh = 62 - bits + (k >> 9);  // k < 512 * (bits + 1): sh <= 63
+        return (w + (1ull << (sh - 1))) >> sh;
     }
     // first-level bin: linear in z, largest first; monotone
     __device__ __forceinline__ int bin0(float x) const {
-        return x == m ? 0 : (int)fminf((m - x) * scale0, (float)(kBins - 1));
+        if (x == m) return 0;
+        return __float_as_int(fminf((m - x) * scale0, (float)(kBins - 1)) + 8388608.f) & (kBins - 1);
     }
 };
 
@@ -168,21 +205,28 @@ struct Cta {
     }
 
     // Bins of one level, of all CTAs: finds the bin where the running count (mass == false)
-    // or mass passes `target`: the first bin with before < target <= before + own.  Returns
+    // or mass passes `target`: the first bin with before < target <= before + own.  share > 0:
+    // the target is that share of all the mass of these bins (returned in `target`).  Returns
     // the bin; before_cnt, before_mass grow by what lies in the bins ahead of it; own: its
     // count and mass.
-    __device__ int find_bin(int b, bool mass, double target, u64& before_cnt, u64& before_mass, u64& own_cnt,
-                            u64& own_mass) {
+    __device__ int find_bin(int b, bool mass, bool with_mass, double share, double& target, u64& before_cnt,
+                            u64& before_mass, u64& own_cnt, u64& own_mass) {
         constexpr int kPer = kBins / kThreads;
         u64 c[kPer], s[kPer], ct = 0, st = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            c[j] = s[j] = 0;
-            const int i = tid * kPer + j;
-            for (unsigned r = 0; r < size; ++r) {
-                c[j] += peer_ld(peer(&sh.cnt[b][i], r));
-                s[j] += peer_ld(peer(&sh.lo[b][i], r)) + ((u64)peer_ld(peer(&sh.hi[b][i], r)) << 32);
+        for (int j = 0; j < kPer; ++j) c[j] = s[j] = 0;
+        for (unsigned r = 0; r < size; ++r) {
+            const uint32_t pc = peer(&sh.cnt[b][tid * kPer], r);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) c[j] += peer_ld(pc + 4 * j);
+            if (with_mass) {
+                const uint32_t pl = peer(&sh.lo[b][tid * kPer], r), ph = peer(&sh.hi[b][tid * kPer], r);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) s[j] += peer_ld(pl + 4 * j) + ((u64)peer_ld(ph + 4 * j) << 32);
             }
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
             ct += c[j];
             st += s[j];
         }
@@ -203,11 +247,15 @@ struct Cta {
         }
         if (tid == 0) sh.pick[0] = kBins;
         __syncthreads();
-        u64 cb = before_cnt + ci - ct, sb = before_mass + si - st;
-        for (int w = 0; w < warp; ++w) {
-            cb += sh.wsum[w];
-            sb += sh.scan[w];
+        u64 cb = before_cnt + ci - ct, sb = before_mass + si - st, all = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) {
+                cb += sh.wsum[w];
+                sb += sh.scan[w];
+            }
+            all += sh.scan[w];
         }
+        if (share > 0.0) target = share * (double)all;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const double lo = mass ? (double)sb : (double)cb, up = mass ? (double)(sb + s[j]) : (double)(cb + c[j]);
@@ -259,16 +307,16 @@ struct Border {
 template <typename Elem, bool RES>
 __device__ Border find_border(Cta<Elem, RES>& t, const Row& row, bool mass, double target, bool with_mass) {
     u64 bc = 0, bm = 0, oc = 0, om = 0;
-    const int b0 = t.find_bin(0, mass, target, bc, bm, oc, om);
+    const int b0 = t.find_bin(0, mass, with_mass, 0.0, target, bc, bm, oc, om);
     Border r;
     r.kt = 0;
     r.c = 0;
     r.equal = 0;
     r.mass = bm + om;
     // the keys that can lie in the bin (its edges, widened by the rounding of bin0)
-    const double w = 1.0 / (double)row.scale0, e = 1e-5 * (b0 + 1) * w + 1e-6 * fabs(row.dm);
+    const double w = 1.0 / (double)row.scale0, e = (1e-5 * (b0 + 1) + 0.51) * w + 1e-6 * fabs(row.dm);
     unsigned khi = b0 == 0 ? key_of(row.m) : min(key_of(row.m), key_of((float)(row.dm - b0 * w + e)));
-    unsigned klo = b0 == kBins - 1 ? key_of(-INFINITY) : key_of((float)(row.dm - (b0 + 1) * w - e));
+    unsigned klo = b0 == kBins - 1 ? key_of(-INFINITY) : key_of((float)(row.dm - b0 * w - e));
     if (isinf(row.m)) {
         khi = key_of(row.m);
         klo = key_of(-INFINITY);
@@ -320,7 +368,7 @@ __device__ Border find_border(Cta<Elem, RES>& t, const Row& row, bool mass, doub
             if (inside(x, k)) t.add_bin(b, (int)((khi - k) >> shift), with_mass ? row.weight(x) : 0ull);
         });
         cluster_sync();
-        const int i = t.find_bin(b, mass, target, bc, bm, oc, om);
+        const int i = t.find_bin(b, mass, with_mass, 0.0, target, bc, bm, oc, om);
         const unsigned top = khi - ((unsigned)i << shift);
         const unsigned span = (1u << shift) - 1;
         if (i >= kBins) {  // cannot be: the bins hold what the bin before held
@@ -332,6 +380,24 @@ __device__ Border find_border(Cta<Elem, RES>& t, const Row& row, bool mass, doub
     }
 }
 
+// Sums over the list's n tokens, two threads for each: f(token) -> (count, mass) terms for
+// this thread's token, of every other one.  Counting all pairs takes n/2 steps of some ten
+// instructions (3 us at the list's full size); it needs no sort and no barrier.
+template <typename F>
+__device__ __forceinline__ void list_sums(const Shared& sh, int n, int tid, unsigned& count, u64& mass, F&& f) {
+    count = 0;
+    mass = 0;
+    for (int i = tid & 1; i < n; i += 2) {
+        const Item o = sh.list[i];
+        if (f(o)) {
+            ++count;
+            mass += o.w;
+        }
+    }
+    count += __shfl_xor_sync(0xffffffffu, count, 1);
+    mass += __shfl_xor_sync(0xffffffffu, mass, 1);
+}
+
 template <typename Elem, bool RES>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleArgs a) {
     extern __shared__ __align__(16) char smem[];
@@ -340,6 +406,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     const int r = blockIdx.x / size;
     Cta<Elem, RES> t{a, sh, reinterpret_cast<float*>(smem + sizeof(Shared)), nullptr, 0, cluster_rank(), size,
                      (int)threadIdx.x, (int)threadIdx.x / 32, (int)threadIdx.x % 32};
+    if (t.tid == 0) sh.listed = 0;
     cluster_arrive();  // waited for before the first word to another CTA: by then all have started
     const int v0 = t.rank * a.per;
     t.z = reinterpret_cast<const Elem*>(a.z) + r * a.row_stride + v0;
@@ -365,6 +432,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             }
         }
     }
+    t.clear_bins(0);
+    for (int i = t.tid; i < kPow; i += kThreads) sh.pow2[i] = (unsigned)(exp2(-i / (double)kPow) * 2147483648.0 + 0.5);
     mi = mi == 0x7fffffff ? mi : mi + v0;
     auto better = [&](float x, int i) {
         if (x > mx || (x == mx && i < mi)) {
@@ -382,7 +451,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         sh.wmax[t.warp] = mx;
         sh.widx[t.warp] = mi;
     }
-    t.clear_bins(0);
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) better(sh.wmax[w], sh.widx[w]);
     cluster_wait();
@@ -390,22 +458,36 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         const Msg* g = t.exchange(0, mx, mi);
         for (unsigned i = 0; i < size; ++i) better(g[i].mx, g[i].idx);
     }
-    const bool writer = t.rank == 0 && t.tid == 0;
-    // Every CTA of the cluster takes the same way out; the last barrier keeps shared memory
-    // alive for the others' reads.
+    // Every CTA of the cluster takes the same way out; a CTA leaves only when no other will
+    // read or write its shared memory any more.
     if (mx == -INFINITY || !(T > 0.f) || k == 1 || mp > 1.f || p <= 0.f) {
-        if (writer) {
+        if (t.rank == 0 && t.tid == 0) {
             a.token[r] = mx == -INFINITY ? -1 : mi;
             if (a.logprob) a.logprob[r] = mx == -INFINITY ? -INFINITY : 0.f;
         }
-        cluster_sync();
-        return;
+        return;  // the exchange's barrier was the last word to any CTA
     }
     Row row;
     row.m = mx;
     row.dm = mx;
     row.it = 1.0 / (double)T;
+    const double c = 1.4426950408889634074 / (double)T;
+    row.c_hi = (float)c;
+    row.c_lo = isinf(row.c_hi) ? 0.f : (float)(c - (double)row.c_hi);
     row.scale0 = fminf(fmaxf((float)kBins / (kRange * T), 1e-30f), 1e30f);
+    row.bits = a.bits;
+    row.pow2 = sh.pow2;
+    const double one = (double)(1ull << a.bits);
+    const double low = mp > 0.f ? log((double)mp) * (double)T : -INFINITY;  // min-p, as a bound on z - m
+    auto min_p_keeps = [&](float x) { return x == row.m || (double)x - row.dm >= low; };
+    const float u = __ldg(a.u + r);
+    // u outside [0, 1) is taken as its nearer end (at 1: the last token with weight)
+    const double uu = fmin(u > 0.f ? (double)u : 0.0, 1.0 - 0x1p-50);
+    auto logprob_of = [&](float x, double W) {
+        return (float)((x == row.m ? 0.0 : ((double)x - row.dm) * row.it) - log(W / one));
+    };
+    // at u below the resolution, the first kept token of any weight at all
+    auto any_weight = [&](float x) { return x == row.m || ((double)x - row.dm) * row.it > -745.0; };
 
     // ---- the border of top-k and top-p
     const bool need_k = k > 0 && k < a.V, need_p = p < 1.f;
@@ -413,77 +495,173 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     bd.kt = 0;
     bd.c = 0;
     bd.equal = 0;
+    int last_equal = 0x7fffffff;  // of the tokens at the border, the last index that is in
     if (need_k || need_p) {
-        unsigned last = 0;  // tokens of the last bin, most of them: counted apart
-        t.each([&](int, float x) {
-            const int b = row.bin0(x);
-            const u64 w = need_p ? row.weight(x) : 0ull;
-            if (b == kBins - 1 && w == 0) ++last;
-            else t.add_bin(0, b, w);
-        });
+        const bool mass0 = need_p && !need_k;  // with top-k, weights count among the first k only
+        auto fill = [&](bool with_mass) {
+            unsigned last = 0;  // tokens of the last bin, most of them: counted apart
+            t.each([&](int, float x) {
+                const int b = row.bin0(x);
+                const u64 w = with_mass ? row.weight(x) : 0ull;
+                if (b == kBins - 1 && w == 0) ++last;
+                else t.add_bin(0, b, w);
+            });
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(0xffffffffu, last, o);
-        if (t.lane == 0 && last) atomicAdd(&sh.cnt[0][kBins - 1], last);
-        u64 total = 0;
-        if (need_p) {
+            for (int o = 16; o > 0; o >>= 1) last += __shfl_xor_sync(0xffffffffu, last, o);
+            if (t.lane == 0 && last) atomicAdd(&sh.cnt[0][kBins - 1], last);
+        };
+        fill(mass0);
+        cluster_sync();
+        u64 bc = 0, bm = 0, oc = 0, om = 0;
+        double target = (double)k;
+        const int b0 = t.find_bin(0, !need_k, mass0, need_k ? 0.0 : (double)p, target, bc, bm, oc, om);
+        const bool whole = bc + oc <= kList;  // all tokens down to the border's bin fit the list
+        if (whole || (mass0 && oc <= kList)) {
+            // Places in the list: one word to the first CTA per CTA, then all tokens at once.
+            auto listed = [&](float x) {
+                const int b = row.bin0(x);
+                return b == b0 || (whole && b < b0);
+            };
+            unsigned hits = 0;
+            t.each([&](int, float x) { hits += listed(x); });
+            unsigned at = hits;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned x = __shfl_up_sync(0xffffffffu, at, o);
+                if (t.lane >= o) at += x;
+            }
+            if (t.lane == 31) sh.widx[t.warp] = (int)at;
             __syncthreads();
-            u64 s = 0;
-            for (int i = t.tid; i < kBins; i += kThreads) s += sh.lo[0][i] + ((u64)sh.hi[0][i] << 32);
-            s = t.block_sum(s);
-            const Msg* g = t.exchange(s, 0.f, 0);
-            for (unsigned i = 0; i < size; ++i) total += g[i].sum;
-        } else {
-            cluster_sync();
-        }
-        if (need_k) {
-            bd = find_border(t, row, false, (double)k, need_p);
-            total = bd.mass;
-        }
-        if (need_p) bd = find_border(t, row, true, (double)p * (double)total, true);
-    }
-    // ---- of the tokens at the border, the first c in index order: the last one's index
-    int last_equal = 0x7fffffff;
-    if (bd.c > 0 && bd.c < bd.equal) {
-        u64 n = 0;
-        t.each([&](int, float x) { n += key_of(x) == bd.kt; });
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        const u64 mine = n;
-        const u64 all = t.block_sum(t.lane == 0 ? n : 0ull);
-        const Msg* g = t.exchange(all, 0.f, 0);
-        u64 before = 0;
-        for (unsigned i = 0; i < t.rank; ++i) before += g[i].sum;
-        for (int w = 0; w < t.warp; ++w) before += sh.wsum[w];
-        int found = 0x7fffffff;
-        if (before < bd.c && bd.c <= before + mine) {
-            const int e = min(t.n, (t.warp + 1) * a.seg);
-            for (int i0 = t.warp * a.seg; i0 < e; i0 += 32) {
-                const int i = i0 + t.lane;
-                const unsigned hit = __ballot_sync(0xffffffffu, i < e && key_of(t.get(i)) == bd.kt);
-                const u64 want = bd.c - before;  // >= 1
-                if (want <= (u64)__popc(hit)) {
-                    unsigned rest = hit;
-                    for (u64 j = 1; j < want; ++j) rest &= rest - 1;
-                    found = v0 + i0 + __ffs(rest) - 1;
-                    break;
+            at -= hits;
+            unsigned all = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < t.warp) at += sh.widx[w];
+                all += sh.widx[w];
+            }
+            if (t.tid == 0) {
+                unsigned first = 0;
+                if (all)
+                    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(first) : "r"(peer(&sh.listed, 0)), "r"(all)
+                                 : "memory");
+                sh.token = first;
+            }
+            __syncthreads();
+            at += sh.token;
+            if (hits)
+                for (int i = t.warp * a.seg + t.lane, e = min(t.n, (t.warp + 1) * a.seg); i < e; i += 32) {
+                    const float x = t.get(i);
+                    if (!listed(x)) continue;
+                    const u64 w = row.weight(x);
+                    const uint32_t d = peer(sh.list + min(at++, kList - 1u), 0);
+                    peer_st(d, key_of(x));
+                    peer_st(d + 4, (unsigned)(v0 + i));
+                    peer_st(d + 8, (unsigned)w);
+                    peer_st(d + 12, (unsigned)(w >> 32));
                 }
-                before += __popc(hit);
+            cluster_sync();
+            const int n = (int)(whole ? bc + oc : oc), me = t.tid >> 1;
+            const bool on = me < n, lead = on && !(t.tid & 1);
+            Item it;
+            unsigned rank = 0;
+            u64 ahead = 0;
+            if (t.rank == 0) {
+                it = sh.list[me];
+                list_sums(sh, n, t.tid, rank, ahead,
+                          [&](const Item& o) { return o.key > it.key || (o.key == it.key && o.idx < it.idx); });
+            }
+            if (whole) {
+                // -------- the first CTA ranks them and draws
+                if (t.rank != 0) return;
+                __syncthreads();  // the list changes below
+                bool in = on && (!need_k || rank < (unsigned)k);
+                if (need_k) target = (double)p * (double)t.block_sum(lead && in ? it.w : 0ull);
+                in = in && (!need_p || rank == 0 || (double)ahead < target) && min_p_keeps(logit_of(it.key));
+                if (lead && !in) sh.list[me].idx = 0xffffffffu;  // out
+                if (t.tid == 0) sh.token = 0xffffffffu;
+                const u64 W = t.block_sum(lead && in ? it.w : 0ull);  // its barriers order the list's changes too
+                const double goal = uu * (double)W;
+                unsigned cnt;
+                u64 run;
+                list_sums(sh, n, t.tid, cnt, run, [&](const Item& o) { return o.idx <= it.idx; });
+                if (lead && in && (goal < 1.0 ? any_weight(logit_of(it.key)) : (double)run > goal)) atomicMin(&sh.token, it.idx);
+                __syncthreads();
+                if (lead && in && it.idx == sh.token) {
+                    a.token[r] = (int)it.idx;
+                    if (a.logprob) a.logprob[r] = logprob_of(logit_of(it.key), (double)W);
+                }
+                return;
+            }
+            // -------- top-p: the last token kept, of the border's bin, to all CTAs
+            if (t.rank == 0) {
+                const bool in = on && (bc + rank == 0 || (double)(bm + ahead) < target);
+                if (t.tid == 0) sh.token = 0;
+                __syncthreads();
+                if (lead && in) atomicMax(&sh.token, rank + 1);
+                __syncthreads();
+                if (lead && rank + 1 == sh.token)
+                    for (unsigned i = 0; i < size; ++i) {
+                        const uint32_t d = peer(&sh.pick[5], i);
+                        peer_st(d, it.key);
+                        peer_st(d + 4, it.idx);
+                    }
+            }
+            cluster_sync();
+            bd.kt = (unsigned)sh.pick[5];
+            bd.c = 1;
+            last_equal = (int)(sh.pick[5] >> 32);
+        } else {
+            // -------- many tokens in the border's bin, or a large k
+            if (need_k && need_p) {  // now with the weights
+                cluster_sync();
+                t.clear_bins(0);
+                __syncthreads();
+                fill(true);
+                cluster_sync();
+            }
+            if (need_k) bd = find_border(t, row, false, (double)k, need_p);
+            if (need_p) bd = find_border(t, row, true, need_k ? (double)p * (double)bd.mass : target, true);
+            if (bd.c > 0 && bd.c < bd.equal) {
+                u64 n = 0;
+                t.each([&](int, float x) { n += key_of(x) == bd.kt; });
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+                const u64 mine = n;
+                const u64 all = t.block_sum(t.lane == 0 ? n : 0ull);
+                const Msg* g = t.exchange(all, 0.f, 0);
+                u64 before = 0;
+                for (unsigned i = 0; i < t.rank; ++i) before += g[i].sum;
+                for (int w = 0; w < t.warp; ++w) before += sh.wsum[w];
+                int found = 0x7fffffff;
+                if (before < bd.c && bd.c <= before + mine) {
+                    const int e = min(t.n, (t.warp + 1) * a.seg);
+                    for (int i0 = t.warp * a.seg; i0 < e; i0 += 32) {
+                        const int i = i0 + t.lane;
+                        const unsigned hit = __ballot_sync(0xffffffffu, i < e && key_of(t.get(i)) == bd.kt);
+                        const u64 want = bd.c - before;  // >= 1
+                        if (want <= (u64)__popc(hit)) {
+                            unsigned rest = hit;
+                            for (u64 j = 1; j < want; ++j) rest &= rest - 1;
+                            found = v0 + i0 + __ffs(rest) - 1;
+                            break;
+                        }
+                        before += __popc(hit);
+                    }
+                }
+                __syncthreads();
+                if (t.lane == 0) sh.widx[t.warp] = found;
+                __syncthreads();
+                for (int w = 0; w < kWarps; ++w) found = min(found, sh.widx[w]);
+                const Msg* h = t.exchange(0, 0.f, found);
+                for (unsigned i = 0; i < size; ++i) last_equal = min(last_equal, h[i].idx);
             }
         }
-        __syncthreads();
-        if (t.lane == 0) sh.widx[t.warp] = found;
-        __syncthreads();
-        for (int w = 0; w < kWarps; ++w) found = min(found, sh.widx[w]);
-        const Msg* h = t.exchange(0, 0.f, found);
-        for (unsigned i = 0; i < size; ++i) last_equal = min(last_equal, h[i].idx);
     }
-    const double low = mp > 0.f ? log((double)mp) * (double)T : -INFINITY;
     auto kept = [&](int i, float x) {
         const unsigned q = key_of(x);
-        const bool in = q > bd.kt || (bd.c > 0 && q == bd.kt && v0 + i <= last_equal) || !(need_k || need_p);
-        return in && (x == row.m || (double)x - row.dm >= low);
+        const bool in = !(need_k || need_p) || q > bd.kt || (bd.c > 0 && q == bd.kt && v0 + i <= last_equal);
+        return in && min_p_keeps(x);
     };
-    // ---- the draw
+    // ---- the draw: all CTAs sum what is kept, in index order
     u64 s = 0;
     t.each([&](int i, float x) {
         if (kept(i, x)) s += row.weight(x);
@@ -499,19 +677,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         W += g[i].sum;
     }
     for (int w = 0; w < t.warp; ++w) before += sh.wsum[w];
-    const float u = __ldg(a.u + r);
-    // u outside [0, 1) is taken as its nearer end (at 1: the last token with weight)
-    const double goal = fmin(u > 0.f ? (double)u : 0.0, 1.0 - 0x1p-50) * (double)W;
+    const double goal = uu * (double)W;
     auto emit = [&](int i) {
         a.token[r] = v0 + i;
-        const double y = ((double)t.get(i) - row.dm) * row.it;
-        if (a.logprob) a.logprob[r] = (float)((t.get(i) == row.m ? 0.0 : y) - log((double)W / kOne));
+        if (a.logprob) a.logprob[r] = logprob_of(t.get(i), (double)W);
     };
     if (goal < 1.0) {
-        // u below the resolution: the first kept token of any weight at all
         int first = 0x7fffffff;
         t.each([&](int i, float x) {
-            if (kept(i, x) && (x == row.m || ((double)x - row.dm) * row.it > -745.0)) first = min(first, i);
+            if (kept(i, x) && any_weight(x)) first = min(first, i);
         });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
@@ -547,7 +721,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
     }
-    cluster_sync();
 }
 
 template <typename Elem, bool RES>
@@ -590,6 +763,7 @@ cudaError_t launch_sample(int nrows, int V, const void* z, int bf16, int64_t row
     a.min_p = min_p;
     a.token = token;
     a.logprob = logprob;
+    a.bits = V <= (1 << 17) ? 46 : 40;
     int cluster = 1;
     while (cluster < kMaxCluster && V > cluster * 2048) cluster *= 2;
     a.per = (V + cluster - 1) / cluster;

@@ -67,6 +67,28 @@ struct Msg {
     int idx;
 };
 
+// 2^31 * 2^(-i / 512), by repeated multiplication with 2^(-1/512) in 64 bits.
+struct PowTable {
+    unsigned v[kPow];
+};
+constexpr u64 mul_high(u64 a, u64 b) {
+    const u64 al = a & 0xffffffffull, ah = a >> 32, bl = b & 0xffffffffull, bh = b >> 32;
+    const u64 mid = ah * bl + ((al * bl) >> 32), mid2 = al * bh + (mid & 0xffffffffull);
+    return ah * bh + (mid >> 32) + (mid2 >> 32);
+}
+constexpr PowTable make_pow_table() {
+    PowTable t{};
+    const u64 step = 18421787711448657618ull;  // 2^64 * 2^(-1/512)
+    u64 x = step;
+    t.v[0] = 0x80000000u;
+    for (int i = 1; i < kPow; ++i) {
+        t.v[i] = (unsigned)((x + (1ull << 32)) >> 33);
+        x = mul_high(x, step);
+    }
+    return t;
+}
+__device__ const PowTable kPowTable = make_pow_table();
+
 struct Shared {
     unsigned cnt[2][kBins], lo[2][kBins], hi[2][kBins];  // bins: tokens, mass (low and high words)
     Item list[kList];
@@ -101,18 +123,34 @@ __device__ __forceinline__ uint32_t peer(const void* p, unsigned rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ unsigned peer_ld(uint32_t a) {
-    unsigned x;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+__device__ __forceinline__ uint2 peer_ld2(uint32_t a) {
+    uint2 x;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
     return x;
 }
 __device__ __forceinline__ void peer_st(uint32_t a, unsigned x) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
 
-__device__ __forceinline__ float to_logit(float x) { return x != x ? -INFINITY : x + 0.f; }  // NaN: never drawn; -0 = 0
+// NaN is never drawn; -0 is 0; +inf counts as the largest finite value.
+__device__ __forceinline__ float to_logit(float x) { return x != x ? -INFINITY : fminf(x, 3.402823466e38f) + 0.f; }
 __device__ __forceinline__ float load_logit(const float* z, int64_t i) { return to_logit(__ldg(z + i)); }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* z, int64_t i) { return to_logit(__bfloat162float(z[i])); }
+// The logits of 16 bytes.
+__device__ __forceinline__ void unpack(const uint4& v, const float*, float* x) {
+    x[0] = __uint_as_float(v.x);
+    x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z);
+    x[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(const uint4& v, const __nv_bfloat16*, float* x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
 
 // The bit pattern of a logit as an integer of the same order.
 __device__ __forceinline__ unsigned key_of(float x) {
@@ -135,7 +173,6 @@ struct Row {
     // q = 1 - 2^-r = a - a^2/2 + a^3/6 for a = r ln 2, |a| < 2^-10.5: the next term is below
     // 2^-46, q is held to 2^-32 and the table to 2^-32.
     __device__ __forceinline__ u64 weight(float x) const {
-        if (x == m) return 1ull << bits;
         const float hi = m - x, bb = hi - m, lo = (m - (hi - bb)) - (x + bb);
         const float p = hi * c_hi;
         if (!(p < (float)(bits + 1))) return 0ull;  // also -inf
@@ -153,7 +190,6 @@ struct Row {
     }
     // first-level bin: linear in z, largest first; monotone
     __device__ __forceinline__ int bin0(float x) const {
-        if (x == m) return 0;
         return __float_as_int(fminf((m - x) * scale0, (float)(kBins - 1)) + 8388608.f) & (kBins - 1);
     }
 };
@@ -215,14 +251,31 @@ struct Cta {
         u64 c[kPer], s[kPer], ct = 0, st = 0;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) c[j] = s[j] = 0;
-        for (unsigned r = 0; r < size; ++r) {
-            const uint32_t pc = peer(&sh.cnt[b][tid * kPer], r);
+        // all loads on their way before the first is added
+        static_assert(kPer == 2, "8-byte loads");
+        uint2 v[kMaxCluster];
+        auto read = [&](const unsigned* from) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) c[j] += peer_ld(pc + 4 * j);
-            if (with_mass) {
-                const uint32_t pl = peer(&sh.lo[b][tid * kPer], r), ph = peer(&sh.hi[b][tid * kPer], r);
+            for (unsigned r = 0; r < kMaxCluster; ++r) v[r] = r < size ? peer_ld2(peer(from + tid * kPer, r)) : make_uint2(0, 0);
+        };
+        read(sh.cnt[b]);
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) s[j] += peer_ld(pl + 4 * j) + ((u64)peer_ld(ph + 4 * j) << 32);
+        for (unsigned r = 0; r < kMaxCluster; ++r) {
+            c[0] += v[r].x;
+            c[1] += v[r].y;
+        }
+        if (with_mass) {
+            read(sh.lo[b]);
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) {
+                s[0] += v[r].x;
+                s[1] += v[r].y;
+            }
+            read(sh.hi[b]);
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) {
+                s[0] += (u64)v[r].x << 32;
+                s[1] += (u64)v[r].y << 32;
             }
         }
 #pragma unroll
@@ -317,10 +370,6 @@ __device__ Border find_border(Cta<Elem, RES>& t, const Row& row, bool mass, doub
     const double w = 1.0 / (double)row.scale0, e = (1e-5 * (b0 + 1) + 0.51) * w + 1e-6 * fabs(row.dm);
     unsigned khi = b0 == 0 ? key_of(row.m) : min(key_of(row.m), key_of((float)(row.dm - b0 * w + e)));
     unsigned klo = b0 == kBins - 1 ? key_of(-INFINITY) : key_of((float)(row.dm - b0 * w - e));
-    if (isinf(row.m)) {
-        khi = key_of(row.m);
-        klo = key_of(-INFINITY);
-    }
     if (klo > khi) klo = khi;
     auto inside = [&](float x, unsigned k) { return k >= klo && k <= khi && row.bin0(x) == b0; };
     while (true) {
@@ -420,27 +469,62 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     // ---- the slice, and the largest logit (lowest index on ties)
     float mx = -INFINITY;
     int mi = 0x7fffffff;
-    {
-        const int e = min(t.n, (t.warp + 1) * a.seg);
-#pragma unroll 8
-        for (int i = t.warp * a.seg + t.lane; i < e; i += 32) {
-            const float x = load_logit(t.z, i);
-            if (RES) t.sx[i] = x;
-            if (x > mx) {
-                mx = x;
-                mi = i;
-            }
-        }
-    }
-    t.clear_bins(0);
-    for (int i = t.tid; i < kPow; i += kThreads) sh.pow2[i] = (unsigned)(exp2(-i / (double)kPow) * 2147483648.0 + 0.5);
-    mi = mi == 0x7fffffff ? mi : mi + v0;
     auto better = [&](float x, int i) {
         if (x > mx || (x == mx && i < mi)) {
             mx = x;
             mi = i;
         }
     };
+    if (RES) {
+        // 16 bytes at a time from the first aligned address; token i goes to sx[i], which is
+        // laid so that an aligned 16 bytes of logits meets aligned shared memory
+        constexpr int kV = 16 / sizeof(Elem);
+        const int pad = (int)(((uintptr_t)t.z & 15) / sizeof(Elem)), i0 = min(t.n, (kV - pad) % kV), nv = (t.n - i0) / kV;
+        t.sx += pad;
+        const uint4* src = reinterpret_cast<const uint4*>(t.z + i0);
+        auto take = [&](const uint4& q, int j) {
+            float x[kV];
+            unpack(q, (const Elem*)nullptr, x);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                x[e] = to_logit(x[e]);
+                if (x[e] > mx) {
+                    mx = x[e];
+                    mi = i0 + j * kV + e;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kV; e += 4)
+                *reinterpret_cast<float4*>(t.sx + i0 + j * kV + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        };
+        int j = t.tid;
+        for (; j + 3 * kThreads < nv; j += 4 * kThreads) {
+            const uint4 q0 = __ldg(src + j), q1 = __ldg(src + j + kThreads), q2 = __ldg(src + j + 2 * kThreads),
+                        q3 = __ldg(src + j + 3 * kThreads);
+            take(q0, j);
+            take(q1, j + kThreads);
+            take(q2, j + 2 * kThreads);
+            take(q3, j + 3 * kThreads);
+        }
+        for (; j < nv; j += kThreads) take(__ldg(src + j), j);
+        const int rest = t.n - nv * kV;  // before the first and after the last 16 bytes
+        if (t.tid < rest) {
+            const int i = t.tid < i0 ? t.tid : t.tid + nv * kV;
+            const float x = load_logit(t.z, i);
+            t.sx[i] = x;
+            better(x, i);
+        }
+    } else {
+        t.each([&](int i, float x) {
+            if (x > mx) {
+                mx = x;
+                mi = i;
+            }
+        });
+    }
+    t.clear_bins(0);
+    for (int i = t.tid; i < kPow; i += kThreads) sh.pow2[i] = kPowTable.v[i];
+    mi = mi == 0x7fffffff ? mi : mi + v0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float x = __shfl_xor_sync(0xffffffffu, mx, o);
@@ -472,14 +556,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     row.dm = mx;
     row.it = 1.0 / (double)T;
     const double c = 1.4426950408889634074 / (double)T;
-    row.c_hi = (float)c;
-    row.c_lo = isinf(row.c_hi) ? 0.f : (float)(c - (double)row.c_hi);
+    row.c_hi = fminf((float)c, 1e30f);
+    row.c_lo = c < 1e30 ? (float)(c - (double)row.c_hi) : 0.f;
     row.scale0 = fminf(fmaxf((float)kBins / (kRange * T), 1e-30f), 1e30f);
     row.bits = a.bits;
     row.pow2 = sh.pow2;
     const double one = (double)(1ull << a.bits);
     const double low = mp > 0.f ? log((double)mp) * (double)T : -INFINITY;  // min-p, as a bound on z - m
-    auto min_p_keeps = [&](float x) { return x == row.m || (double)x - row.dm >= low; };
+    const float least = mp > 0.f ? fminf(__double2float_ru(row.dm + low), row.m) : -INFINITY;
+    auto min_p_keeps = [&](float x) { return x >= least; };
     const float u = __ldg(a.u + r);
     // u outside [0, 1) is taken as its nearer end (at 1: the last token with weight)
     const double uu = fmin(u > 0.f ? (double)u : 0.0, 1.0 - 0x1p-50);
@@ -656,9 +741,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
             }
         }
     }
+    // the border as a logit (nothing lies between the keys of -0, which no token has, and of
+    // the negative number nearest 0; tokens at -inf weigh nothing)
+    const float border = bd.kt == 0x7fffffffu ? __uint_as_float(0x80000001u) : bd.kt <= 0x007fffffu ? -INFINITY : logit_of(bd.kt);
     auto kept = [&](int i, float x) {
-        const unsigned q = key_of(x);
-        const bool in = !(need_k || need_p) || q > bd.kt || (bd.c > 0 && q == bd.kt && v0 + i <= last_equal);
+        const bool in = !(need_k || need_p) || x > border || (bd.c > 0 && x == border && v0 + i <= last_equal);
         return in && min_p_keeps(x);
     };
     // ---- the draw: all CTAs sum what is kept, in index order
@@ -738,7 +825,7 @@ cudaError_t launch_t(SampleArgs a, int cluster, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.nrows * cluster));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared) + (RES ? (size_t)a.per * 4 : 0);
+    cfg.dynamicSmemBytes = sizeof(Shared) + (RES ? (size_t)a.per * 4 + 32 : 0);
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
@@ -766,9 +853,9 @@ cudaError_t launch_sample(int nrows, int V, const void* z, int bf16, int64_t row
     a.bits = V <= (1 << 17) ? 46 : 40;
     int cluster = 1;
     while (cluster < kMaxCluster && V > cluster * 2048) cluster *= 2;
-    a.per = (V + cluster - 1) / cluster;
+    a.per = ((V + cluster - 1) / cluster + 7) / 8 * 8;  // slices begin alike against 16 bytes
     a.seg = (a.per + 32 * kWarps - 1) / (32 * kWarps) * 32;
-    const bool res = sizeof(Shared) + (size_t)a.per * 4 <= 232448;
+    const bool res = sizeof(Shared) + (size_t)a.per * 4 + 32 <= 232448;
     if (bf16) return res ? launch_t<__nv_bfloat16, true>(a, cluster, st) : launch_t<__nv_bfloat16, false>(a, cluster, st);
     return res ? launch_t<float, true>(a, cluster, st) : launch_t<float, false>(a, cluster, st);
 }

@@ -95,6 +95,23 @@ def test_ties_keep_the_lowest_index():
     assert list(check(z, u, None, np.full(4, 3, np.int32), np.full(4, 0.5, np.float32))) == [0, 0, 1, 1]
 
 
+def test_border_at_zero_and_at_minus_infinity():
+    rng = np.random.default_rng(11)
+    n, V = 6, 6000
+    z = -np.abs(rng.standard_normal((n, V))).astype(np.float32) - 0.01
+    z[:, 100:900] = 0.0
+    z[:, 500] = -0.0
+    z[:, :50] = 0.5
+    u = rng.random(n).astype(np.float32)
+    for k in (49, 50, 51, 849, 850, 851, 2000):
+        check(z, u, None, np.full(n, k, np.int32))
+        check(z, 1 - u / 100, None, np.full(n, k, np.int32), np.full(n, 0.99, np.float32))
+    z[:, 2000:] = -np.inf
+    for k in (1999, 2000, 2001, 5999):
+        check(z, 1 - u / 1000, None, np.full(n, k, np.int32))
+        check(z, 1 - u / 1000, None, np.full(n, k, np.int32), np.full(n, 0.999, np.float32))
+
+
 def test_extreme_settings():
     rng = np.random.default_rng(5)
     n, V = 8, 3000

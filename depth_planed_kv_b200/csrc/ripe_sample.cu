@@ -17,15 +17,18 @@
 // 10^4 of 10^5 near-equal tokens would draw its neighbour.)
 //
 // One cluster of 1 to 8 CTAs per row; each CTA holds a contiguous slice of the row in
-// shared memory, so the logits are read from memory once.  The order's prefix is found
-// from 1024 bins, linear in z below the maximum, which the CTAs read from one another
-// through distributed shared memory:
-//   - few tokens down to the border's bin (most rows): they are gathered in the first
-//     CTA, ranked there by counting, and drawn from; the other CTAs are done;
-//   - top-p over a flatter row: the border's bin alone is gathered and ranked, then all
-//     CTAs sum what is kept;
-//   - else (a bin of many tokens): bins of the ordered bit pattern inside the border's
-//     bin, until it holds one token or one value.
+// shared memory, so the logits are read from memory once.
+//   top-k up to a few hundred (the usual case): each CTA's threads have the largest logit
+//     of their share; the ceil(k / CTAs)-th largest of those is a bound that so many of the
+//     CTA's tokens reach, so the least such bound of the CTAs is reached by k tokens of the
+//     row, and by few more.  Those alone are gathered in the first CTA, sorted and drawn
+//     from; the other CTAs are done.
+//   top-p: 1024 bins of tokens and mass, linear in z below the maximum, which the CTAs
+//     read from one another through distributed shared memory, give the bin where the mass
+//     passes p.  The tokens down to it, if few, are gathered as above; else the border's
+//     bin alone is gathered and sorted, and then all CTAs sum what is kept.
+//   else (many tokens in that bin, or a large k): bins of the ordered bit pattern inside
+//     the border's bin, until it holds one token or one value.
 #include <math.h>
 
 #include "ripe_internal.cuh"
@@ -36,7 +39,7 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kMaxCluster = 8;
-constexpr int kList = kThreads / 2;  // tokens ranked in one CTA, two threads each
+constexpr int kList = kThreads;  // tokens sorted in one CTA
 constexpr float kRange = 28.f;  // the bins reach this many units of T below the maximum
 constexpr int kPow = 512;       // table of 2^(-i / 512)
 
@@ -53,16 +56,10 @@ struct SampleArgs {
     int bits;  // the largest weight is 2^bits
 };
 
-// A gathered token.
-struct alignas(16) Item {
-    unsigned key, idx;
-    u64 w;
-};
-
 // What a CTA tells the others of its cluster; two of them in turn, so that one cluster
 // barrier per exchange is enough.
-struct Msg {
-    u64 sum;
+struct alignas(16) Msg {
+    u64 sum;  // or a key
     float mx;
     int idx;
 };
@@ -91,7 +88,9 @@ __device__ const PowTable kPowTable = make_pow_table();
 
 struct Shared {
     unsigned cnt[2][kBins], lo[2][kBins], hi[2][kBins];  // bins: tokens, mass (low and high words)
-    Item list[kList];
+    u64 list[kList];      // gathered tokens: (key, ~index), so that larger comes first
+    u64 swap[kList];
+    unsigned mine[kList];  // this CTA's tokens for the list
     unsigned pow2[kPow];  // 2^31 * 2^(-i / 512)
     Msg msg[2][kMaxCluster];
     u64 wsum[kWarps], scan[kWarps];
@@ -164,28 +163,27 @@ __device__ __forceinline__ float logit_of(unsigned key) {
 
 struct Row {
     float m, scale0;       // maximum; bins per unit of z at the first level
-    float c_hi, c_lo;      // log2(e) / T as a sum of two floats
+    float c_hi, c_lo, c_512;  // log2(e) / T as a sum of two floats, and 512 times it
     double dm, it;         // maximum, 1 / T
     int bits;
     const unsigned* pow2;
-    // 2^bits * exp((x - m) / T), rounded.  t = (m - x) * c as p + e (the difference and the
-    // product each with their rounding error), t = k / 512 + r; 2^-t = 2^(-k / 512) (1 - q),
-    // q = 1 - 2^-r = a - a^2/2 + a^3/6 for a = r ln 2, |a| < 2^-10.5: the next term is below
-    // 2^-46, q is held to 2^-32 and the table to 2^-32.
+    // 2^bits * exp((x - m) / T), rounded.  t = (m - x) * c (the difference with its rounding
+    // error, the product through fused operations), t = k / 512 + r; 2^-t = 2^(-k / 512) (1 - q),
+    // q = 1 - 2^-r = r (ln2 - r (ln2^2 / 2 - r ln2^3 / 6)) for |r| < 2^-9.9: the next term is
+    // below 2^-46, q is held to 2^-32 and the table to 2^-32.
     __device__ __forceinline__ u64 weight(float x) const {
         const float hi = m - x, bb = hi - m, lo = (m - (hi - bb)) - (x + bb);
-        const float p = hi * c_hi;
-        if (!(p < (float)(bits + 1))) return 0ull;  // also -inf
-        const float e = fmaf(hi, c_lo, fmaf(lo, c_hi, fmaf(hi, c_hi, -p)));
         const float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the rounded integer in the low bits
-        const float y = fmaf(p, (float)kPow, kMagic);
-        const int k = __float_as_int(y) - __float_as_int(kMagic);
-        const float a = (fmaf(y - kMagic, -1.f / kPow, p) + e) * 0.693147180559945309f;
-        const float q = a * (1.f - a * (0.5f - a * 0.16666667f));
+        const float p = hi * c_512;
+        if (!(p < (float)(kPow * (bits + 1)))) return 0ull;  // also -inf
+        const float y = p + kMagic, kf = (y - kMagic) * (-1.f / kPow);
+        const float r = fmaf(lo, c_hi, fmaf(hi, c_lo, fmaf(hi, c_hi, kf)));
+        const float q = r * (0.693147181f - r * (0.240226507f - r * 0.0555041087f));
         const int qi = __float_as_int(fmaf(q, 2147483648.f, kMagic)) - __float_as_int(kMagic);
+        const int k = __float_as_int(y) - __float_as_int(kMagic);
         const unsigned T = pow2[k & (kPow - 1)];
         const u64 w = ((u64)T << 31) - (u64)((long long)qi * (long long)T);  // 2^62 * 2^-frac
-        const int sh = 62 - bits + (k >> 9);  // k < 512 * (bits + 1): sh <= 63
+        const int sh = 62 - bits + (k >> 9);  // k <= 512 * (bits + 1): sh <= 63
         return (w + (1ull << (sh - 1))) >> sh;
     }
     // first-level bin: linear in z, largest first; monotone
@@ -212,6 +210,85 @@ struct Cta {
         const int e = min(n, (warp + 1) * a.seg);
 #pragma unroll 4
         for (int i = warp * a.seg + lane; i < e; i += 32) f(i, get(i));
+    }
+
+    // The same in any order, 16 bytes of shared memory at a time (a: where the slice's first
+    // token lies against 16 bytes).
+    template <typename F>
+    __device__ __forceinline__ void each_any(F&& f) const {
+        if (!RES) {
+            each(f);
+            return;
+        }
+        const int off = (int)(((uintptr_t)sx & 15) / 4), i0 = min(n, (4 - off) & 3), nq = (n - i0) / 4;
+#pragma unroll 2
+        for (int q = tid; q < nq; q += kThreads) {
+            const int i = i0 + 4 * q;
+            const float4 v = *reinterpret_cast<const float4*>(sx + i);
+            f(i, v.x);
+            f(i + 1, v.y);
+            f(i + 2, v.z);
+            f(i + 3, v.w);
+        }
+        if (tid < n - 4 * nq) {
+            const int i = tid < i0 ? tid : tid + 4 * nq;
+            f(i, sx[i]);
+        }
+    }
+
+    // Gathers tokens (each CTA's `count` slice indexes in sh.mine) in the first CTA's list, if
+    // they fit; returns how many there are in all.  Ends with a barrier of the cluster.
+    __device__ __forceinline__ unsigned gather(unsigned count, int v0) {
+        const Msg* g = exchange(count, 0.f, 0);
+        unsigned at = 0, all = 0;
+        for (unsigned i = 0; i < size; ++i) {
+            if (i < rank) at += (unsigned)g[i].sum;
+            all += (unsigned)g[i].sum;
+        }
+        if (all > kList) return all;
+        for (unsigned j = tid; j < count; j += kThreads) {
+            const int i = sh.mine[j];
+            const uint32_t d = peer(sh.list + at + j, 0);
+            peer_st(d + 4, key_of(get(i)));
+            peer_st(d, ~(unsigned)(v0 + i));
+        }
+        cluster_sync();
+        return all;
+    }
+
+    // Sorts the CTA's values, one per thread, largest first, where the first `n` count (the
+    // others are 0, which is no token's value).  Bitonic: strides below 32 by shuffles.
+    __device__ __forceinline__ u64 sort(u64 v, int n) {
+        for (int s = 2; s / 2 < n; s *= 2) {
+            const bool down = !(tid & s);
+            for (int d = s / 2; d > 0; d /= 2) {
+                u64 o;
+                if (d < 32) {
+                    o = __shfl_xor_sync(0xffffffffu, v, d);
+                } else {
+                    __syncthreads();
+                    sh.swap[tid] = v;
+                    __syncthreads();
+                    o = sh.swap[tid ^ d];
+                }
+                const bool keep_large = (!(tid & d)) == down;
+                v = keep_large == (v > o) ? v : o;
+            }
+        }
+        return v;
+    }
+    // Sum over the threads before and up to this one.
+    __device__ __forceinline__ u64 inclusive(u64 v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 x = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += x;
+        }
+        __syncthreads();
+        if (lane == 31) sh.wsum[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) v += sh.wsum[w];
+        return v;
     }
 
     // Tells every CTA of the cluster this CTA's (sum, mx, idx), and returns all of them.
@@ -429,26 +506,8 @@ __device__ Border find_border(Cta<Elem, RES>& t, const Row& row, bool mass, doub
     }
 }
 
-// Sums over the list's n tokens, two threads for each: f(token) -> (count, mass) terms for
-// this thread's token, of every other one.  Counting all pairs takes n/2 steps of some ten
-// instructions (3 us at the list's full size); it needs no sort and no barrier.
-template <typename F>
-__device__ __forceinline__ void list_sums(const Shared& sh, int n, int tid, unsigned& count, u64& mass, F&& f) {
-    count = 0;
-    mass = 0;
-    for (int i = tid & 1; i < n; i += 2) {
-        const Item o = sh.list[i];
-        if (f(o)) {
-            ++count;
-            mass += o.w;
-        }
-    }
-    count += __shfl_xor_sync(0xffffffffu, count, 1);
-    mass += __shfl_xor_sync(0xffffffffu, mass, 1);
-}
-
 template <typename Elem, bool RES>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
     extern __shared__ __align__(16) char smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem);
     const unsigned size = cluster_size();
@@ -524,6 +583,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     }
     t.clear_bins(0);
     for (int i = t.tid; i < kPow; i += kThreads) sh.pow2[i] = kPowTable.v[i];
+    const unsigned top = key_of(mx);  // of this thread's tokens
     mi = mi == 0x7fffffff ? mi : mi + v0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -536,11 +596,33 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         sh.widx[t.warp] = mi;
     }
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) better(sh.wmax[w], sh.widx[w]);
+    // ---- top-k: the bound that enough of this CTA's tokens reach (see above), to 16 bits of its key
+    const bool need_k = k > 0 && k < a.V, need_p = p < 1.f, few_k = need_k && k <= kList * 3 / 4;
+    unsigned bound = 0;
+    if (few_k) {
+        const int want = (k + (int)size - 1) / (int)size;
+        for (int bit = 15; bit >= 0; --bit) {
+            const unsigned b = bound | (1u << bit);
+            if (__syncthreads_count((top >> 16) >= b) >= want) bound = b;
+        }
+    }
+    {
+        mx = sh.wmax[t.lane & (kWarps - 1)];
+        mi = sh.widx[t.lane & (kWarps - 1)];
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, mx, o);
+            const int i = __shfl_xor_sync(0xffffffffu, mi, o);
+            better(x, i);
+        }
+    }
     cluster_wait();
     {
-        const Msg* g = t.exchange(0, mx, mi);
-        for (unsigned i = 0; i < size; ++i) better(g[i].mx, g[i].idx);
+        const Msg* g = t.exchange(bound, mx, mi);
+        for (unsigned i = 0; i < size; ++i) {
+            better(g[i].mx, g[i].idx);
+            bound = min(bound, (unsigned)g[i].sum);
+        }
     }
     // Every CTA of the cluster takes the same way out; a CTA leaves only when no other will
     // read or write its shared memory any more.
@@ -557,6 +639,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     row.it = 1.0 / (double)T;
     const double c = 1.4426950408889634074 / (double)T;
     row.c_hi = fminf((float)c, 1e30f);
+    row.c_512 = row.c_hi * kPow;
     row.c_lo = c < 1e30 ? (float)(c - (double)row.c_hi) : 0.f;
     row.scale0 = fminf(fmaxf((float)kBins / (kRange * T), 1e-30f), 1e30f);
     row.bits = a.bits;
@@ -574,18 +657,68 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     // at u below the resolution, the first kept token of any weight at all
     auto any_weight = [&](float x) { return x == row.m || ((double)x - row.dm) * row.it > -745.0; };
 
+    // The first CTA's end of a row whose tokens of interest (n of them) are all in its list.
+    auto draw_from_list = [&](int n, double target) {
+        const u64 v = t.sort(t.tid < n ? sh.list[t.tid] : 0ull, n);
+        const float x = logit_of((unsigned)(v >> 32));
+        const unsigned index = ~(unsigned)v;
+        const u64 w = t.tid < n ? row.weight(x) : 0ull;
+        const u64 upto = t.inclusive(w);
+        bool in = t.tid < n && (!need_k || t.tid < k);
+        if (need_k && need_p) target = (double)p * (double)t.block_sum(in ? w : 0ull);
+        in = in && (!need_p || t.tid == 0 || (double)(upto - w) < target) && min_p_keeps(x);
+        // in index order
+        __syncthreads();
+        sh.list[t.tid] = w;  // by rank
+        if (t.tid == 0) sh.token = 0xffffffffu;
+        const int kept = __syncthreads_count(in);
+        u64 o = t.sort(in ? ((u64)~index << 32 | (unsigned)t.tid) : 0ull, n);
+        const unsigned rank = (unsigned)o & (kList - 1);
+        const bool on = t.tid < kept;
+        const u64 w2 = on ? sh.list[rank] : 0ull, run = t.inclusive(w2);
+        const u64 W = t.block_sum(w2);
+        const double goal = uu * (double)W;
+        sh.swap[t.tid] = (u64)__float_as_uint(x);  // by rank (the sums' barriers came after the sort)
+        __syncthreads();
+        const float y = __uint_as_float((unsigned)sh.swap[rank]);
+        if (on && (goal < 1.0 ? any_weight(y) : (double)run > goal)) atomicMin(&sh.token, (unsigned)t.tid);
+        __syncthreads();
+        if ((unsigned)t.tid == sh.token) {
+            a.token[r] = (int)~(unsigned)(o >> 32);
+            if (a.logprob) a.logprob[r] = logprob_of(y, (double)W);
+        }
+    };
+
     // ---- the border of top-k and top-p
-    const bool need_k = k > 0 && k < a.V, need_p = p < 1.f;
     Border bd;
     bd.kt = 0;
     bd.c = 0;
     bd.equal = 0;
     int last_equal = 0x7fffffff;  // of the tokens at the border, the last index that is in
+    // Slice indexes of the tokens for which f(x), in sh.mine (as many as fit); returns how many.
+    auto collect = [&](auto&& f) -> unsigned {
+        t.each_any([&](int i, float x) {
+            if (f(x)) {
+                const unsigned at = atomicAdd(&sh.listed, 1u);
+                if (at < kList) sh.mine[at] = (unsigned)i;
+            }
+        });
+        __syncthreads();
+        return sh.listed;
+    };
+    if (few_k) {
+        const float from = bound <= 0x007fu ? -INFINITY : logit_of(bound << 16);
+        const unsigned n = t.gather(collect([&](float x) { return x >= from; }), v0);
+        if (n <= kList) {
+            if (t.rank == 0) draw_from_list((int)n, 0.0);
+            return;
+        }
+    }
     if (need_k || need_p) {
         const bool mass0 = need_p && !need_k;  // with top-k, weights count among the first k only
         auto fill = [&](bool with_mass) {
             unsigned last = 0;  // tokens of the last bin, most of them: counted apart
-            t.each([&](int, float x) {
+            t.each_any([&](int, float x) {
                 const int b = row.bin0(x);
                 const u64 w = with_mass ? row.weight(x) : 0ull;
                 if (b == kBins - 1 && w == 0) ++last;
@@ -601,93 +734,30 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         double target = (double)k;
         const int b0 = t.find_bin(0, !need_k, mass0, need_k ? 0.0 : (double)p, target, bc, bm, oc, om);
         const bool whole = bc + oc <= kList;  // all tokens down to the border's bin fit the list
-        if (whole || (mass0 && oc <= kList)) {
-            // Places in the list: one word to the first CTA per CTA, then all tokens at once.
-            auto listed = [&](float x) {
+        if (mass0 && (whole || oc <= kList)) {
+            // a first test that is cheaper than the bin: half a bin and the rounding below it
+            const float from = b0 == kBins - 1 ? -INFINITY
+                                               : (float)(row.dm - (b0 + 0.51 + 1e-5 * b0) / (double)row.scale0 - 1e-6 * fabs(row.dm));
+            const unsigned n = t.gather(collect([&](float x) {
+                if (!(x >= from)) return false;
                 const int b = row.bin0(x);
                 return b == b0 || (whole && b < b0);
-            };
-            unsigned hits = 0;
-            t.each([&](int, float x) { hits += listed(x); });
-            unsigned at = hits;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned x = __shfl_up_sync(0xffffffffu, at, o);
-                if (t.lane >= o) at += x;
-            }
-            if (t.lane == 31) sh.widx[t.warp] = (int)at;
-            __syncthreads();
-            at -= hits;
-            unsigned all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < t.warp) at += sh.widx[w];
-                all += sh.widx[w];
-            }
-            if (t.tid == 0) {
-                unsigned first = 0;
-                if (all)
-                    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(first) : "r"(peer(&sh.listed, 0)), "r"(all)
-                                 : "memory");
-                sh.token = first;
-            }
-            __syncthreads();
-            at += sh.token;
-            if (hits)
-                for (int i = t.warp * a.seg + t.lane, e = min(t.n, (t.warp + 1) * a.seg); i < e; i += 32) {
-                    const float x = t.get(i);
-                    if (!listed(x)) continue;
-                    const u64 w = row.weight(x);
-                    const uint32_t d = peer(sh.list + min(at++, kList - 1u), 0);
-                    peer_st(d, key_of(x));
-                    peer_st(d + 4, (unsigned)(v0 + i));
-                    peer_st(d + 8, (unsigned)w);
-                    peer_st(d + 12, (unsigned)(w >> 32));
-                }
-            cluster_sync();
-            const int n = (int)(whole ? bc + oc : oc), me = t.tid >> 1;
-            const bool on = me < n, lead = on && !(t.tid & 1);
-            Item it;
-            unsigned rank = 0;
-            u64 ahead = 0;
-            if (t.rank == 0) {
-                it = sh.list[me];
-                list_sums(sh, n, t.tid, rank, ahead,
-                          [&](const Item& o) { return o.key > it.key || (o.key == it.key && o.idx < it.idx); });
-            }
+            }), v0);
             if (whole) {
-                // -------- the first CTA ranks them and draws
-                if (t.rank != 0) return;
-                __syncthreads();  // the list changes below
-                bool in = on && (!need_k || rank < (unsigned)k);
-                if (need_k) target = (double)p * (double)t.block_sum(lead && in ? it.w : 0ull);
-                in = in && (!need_p || rank == 0 || (double)ahead < target) && min_p_keeps(logit_of(it.key));
-                if (lead && !in) sh.list[me].idx = 0xffffffffu;  // out
-                if (t.tid == 0) sh.token = 0xffffffffu;
-                const u64 W = t.block_sum(lead && in ? it.w : 0ull);  // its barriers order the list's changes too
-                const double goal = uu * (double)W;
-                unsigned cnt;
-                u64 run;
-                list_sums(sh, n, t.tid, cnt, run, [&](const Item& o) { return o.idx <= it.idx; });
-                if (lead && in && (goal < 1.0 ? any_weight(logit_of(it.key)) : (double)run > goal)) atomicMin(&sh.token, it.idx);
-                __syncthreads();
-                if (lead && in && it.idx == sh.token) {
-                    a.token[r] = (int)it.idx;
-                    if (a.logprob) a.logprob[r] = logprob_of(logit_of(it.key), (double)W);
-                }
+                if (t.rank == 0) draw_from_list((int)n, target);
                 return;
             }
-            // -------- top-p: the last token kept, of the border's bin, to all CTAs
+            // -------- the last token kept, of the border's bin, to all CTAs
             if (t.rank == 0) {
-                const bool in = on && (bc + rank == 0 || (double)(bm + ahead) < target);
-                if (t.tid == 0) sh.token = 0;
-                __syncthreads();
-                if (lead && in) atomicMax(&sh.token, rank + 1);
-                __syncthreads();
-                if (lead && rank + 1 == sh.token)
+                const u64 v = t.sort(t.tid < (int)n ? sh.list[t.tid] : 0ull, (int)n);
+                const u64 w = t.tid < (int)n ? row.weight(logit_of((unsigned)(v >> 32))) : 0ull;
+                const u64 ahead = bm + t.inclusive(w) - w;
+                const int in = __syncthreads_count(t.tid < (int)n && (bc + t.tid == 0 || (double)ahead < target));
+                if (t.tid == in - 1)
                     for (unsigned i = 0; i < size; ++i) {
                         const uint32_t d = peer(&sh.pick[5], i);
-                        peer_st(d, it.key);
-                        peer_st(d + 4, it.idx);
+                        peer_st(d, (unsigned)(v >> 32));
+                        peer_st(d + 4, ~(unsigned)v);
                     }
             }
             cluster_sync();

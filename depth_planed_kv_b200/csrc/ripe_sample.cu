@@ -89,7 +89,7 @@ __device__ const PowTable kPowTable = make_pow_table();
 struct Shared {
     unsigned cnt[2][kBins], lo[2][kBins], hi[2][kBins];  // bins: tokens, mass (low and high words)
     u64 list[kList];      // gathered tokens: (key, ~index), so that larger comes first
-    u64 swap[kList];
+    u64 swap[2 * kList];
     unsigned mine[kList];  // this CTA's tokens for the list
     unsigned pow2[kPow];  // 2^31 * 2^(-i / 512)
     Msg msg[2][kMaxCluster];
@@ -98,6 +98,9 @@ struct Shared {
     int widx[kWarps];
     u64 pick[6];
     unsigned listed, token;
+    unsigned count[2][kMaxCluster];  // tokens each CTA lists
+    double it, c, low;               // the row's settings, see Row
+    int lo16;
 };
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -110,8 +113,9 @@ __device__ __forceinline__ unsigned cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
     return n;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Without .aligned: the loops before a barrier may leave a warp's lanes apart.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
     cluster_arrive();
     cluster_wait();
@@ -236,47 +240,51 @@ struct Cta {
         }
     }
 
-    // Gathers tokens (each CTA's `count` slice indexes in sh.mine) in the first CTA's list, if
-    // they fit; returns how many there are in all.  Ends with a barrier of the cluster.
-    __device__ __forceinline__ unsigned gather(unsigned count, int v0) {
-        const Msg* g = exchange(count, 0.f, 0);
-        unsigned at = 0, all = 0;
-        for (unsigned i = 0; i < size; ++i) {
-            if (i < rank) at += (unsigned)g[i].sum;
-            all += (unsigned)g[i].sum;
-        }
-        if (all > kList) return all;
-        for (unsigned j = tid; j < count; j += kThreads) {
-            const int i = sh.mine[j];
-            const uint32_t d = peer(sh.list + at + j, 0);
-            peer_st(d + 4, key_of(get(i)));
-            peer_st(d, ~(unsigned)(v0 + i));
-        }
+    // Gathers tokens (each CTA's `count` slice indexes in sh.mine) in the first CTA: each CTA
+    // has its own part of the list there, so that one barrier of the cluster does.  False (to
+    // all CTAs) if one has more than its part holds.  In the first CTA the tokens end up in
+    // sh.list[0 .. n).
+    __device__ __forceinline__ bool gather(unsigned count, int v0, int use, int& n) {
+        const unsigned part = 2 * kList / size, most = part < kList ? part : kList;  // sh.mine holds kList
+        if (tid < (int)size) peer_st(peer(&sh.count[use][rank], tid), count);
+        if (count <= most)
+            for (unsigned j = tid; j < count; j += kThreads) {
+                const int i = sh.mine[j];
+                const uint32_t d = peer(sh.swap + rank * part + j, 0);
+                peer_st(d + 4, key_of(get(i)));
+                peer_st(d, ~(unsigned)(v0 + i));
+            }
         cluster_sync();
-        return all;
+        bool fit = true;
+        n = 0;
+        for (unsigned i = 0; i < size; ++i) {
+            const unsigned c = sh.count[use][i];
+            fit &= c <= most;
+            n += (int)c;
+        }
+        fit &= n <= kList;
+        if (rank == 0 && fit) {
+            for (unsigned q = tid; q < 2 * kList; q += kThreads) {
+                const unsigned from = q / part, j = q % part;
+                unsigned at = 0;
+                for (unsigned i = 0; i < from; ++i) at += sh.count[use][i];
+                if (j < sh.count[use][from]) sh.list[at + j] = sh.swap[q];
+            }
+            __syncthreads();
+        }
+        return fit;
     }
 
-    // Sorts the CTA's values, one per thread, largest first, where the first `n` count (the
-    // others are 0, which is no token's value).  Bitonic: strides below 32 by shuffles.
-    __device__ __forceinline__ u64 sort(u64 v, int n) {
-        for (int s = 2; s / 2 < n; s *= 2) {
-            const bool down = !(tid & s);
-            for (int d = s / 2; d > 0; d /= 2) {
-                u64 o;
-                if (d < 32) {
-                    o = __shfl_xor_sync(0xffffffffu, v, d);
-                } else {
-                    __syncthreads();
-                    sh.swap[tid] = v;
-                    __syncthreads();
-                    o = sh.swap[tid ^ d];
-                }
-                const bool keep_large = (!(tid & d)) == down;
-                v = keep_large == (v > o) ? v : o;
-            }
+    // How many of sh.list[0 .. n) are larger than this thread's v: its rank.
+    __device__ __forceinline__ int rank_of(u64 v, int n) const {
+        int k = 0;
+        if (warp * 32 < n) {
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) k += sh.list[i] > v;
         }
-        return v;
+        return k;
     }
+
     // Sum over the threads before and up to this one.
     __device__ __forceinline__ u64 inclusive(u64 v) {
 #pragma unroll
@@ -287,8 +295,11 @@ struct Cta {
         __syncthreads();
         if (lane == 31) sh.wsum[warp] = v;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) v += sh.wsum[w];
-        return v;
+        static_assert(kWarps == 16, "half a warp adds them");
+        u64 s = (lane & 15) < warp ? sh.wsum[lane & 15] : 0ull;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return v + s;
     }
 
     // Tells every CTA of the cluster this CTA's (sum, mx, idx), and returns all of them.
@@ -514,7 +525,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int r = blockIdx.x / size;
     Cta<Elem, RES> t{a, sh, reinterpret_cast<float*>(smem + sizeof(Shared)), nullptr, 0, cluster_rank(), size,
                      (int)threadIdx.x, (int)threadIdx.x / 32, (int)threadIdx.x % 32};
-    if (t.tid == 0) sh.listed = 0;
+    if (t.tid == 0) {
+        sh.listed = 0;
+        sh.lo16 = 0xffff;
+    }
     cluster_arrive();  // waited for before the first word to another CTA: by then all have started
     const int v0 = t.rank * a.per;
     t.z = reinterpret_cast<const Elem*>(a.z) + r * a.row_stride + v0;
@@ -524,6 +538,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int k = a.top_k ? __ldg(a.top_k + r) : 0;
     const float p = a.top_p ? __ldg(a.top_p + r) : 1.f;
     const float mp = a.min_p ? __ldg(a.min_p + r) : 0.f;
+    if (t.tid == kThreads - 1) {  // 64-bit divisions and logarithms once, beside the loads
+        sh.it = 1.0 / (double)T;
+        sh.c = 1.4426950408889634074 * sh.it;
+        sh.low = mp > 0.f ? log((double)mp) * (double)T : -INFINITY;  // min-p, as a bound on z - m
+    }
 
     // ---- the slice, and the largest logit (lowest index on ties)
     float mx = -INFINITY;
@@ -600,11 +619,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const bool need_k = k > 0 && k < a.V, need_p = p < 1.f, few_k = need_k && k <= kList * 3 / 4;
     unsigned bound = 0;
     if (few_k) {
-        const int want = (k + (int)size - 1) / (int)size;
-        for (int bit = 15; bit >= 0; --bit) {
-            const unsigned b = bound | (1u << bit);
-            if (__syncthreads_count((top >> 16) >= b) >= want) bound = b;
-        }
+        const unsigned least16 = __reduce_min_sync(0xffffffffu, top >> 16);
+        if (t.lane == 0) atomicMin(&sh.lo16, (int)least16);
     }
     {
         mx = sh.wmax[t.lane & (kWarps - 1)];
@@ -615,6 +631,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             const int i = __shfl_xor_sync(0xffffffffu, mi, o);
             better(x, i);
         }
+    }
+    if (few_k) {
+        const int want = (k + (int)size - 1) / (int)size;
+        __syncthreads();
+        unsigned lo = sh.lo16, hi = (key_of(mx) >> 16) + 1;  // all of the threads' maxima reach lo, none reaches hi
+        if (want > kThreads) hi = lo + 1;
+        while (hi - lo > 1) {
+            const unsigned mid = (lo + hi) / 2;
+            if (__syncthreads_count((top >> 16) >= mid) >= want) lo = mid; else hi = mid;
+        }
+        bound = lo;
     }
     cluster_wait();
     {
@@ -636,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     Row row;
     row.m = mx;
     row.dm = mx;
-    row.it = 1.0 / (double)T;
-    const double c = 1.4426950408889634074 / (double)T;
+    row.it = sh.it;
+    const double c = sh.c;
     row.c_hi = fminf((float)c, 1e30f);
     row.c_512 = row.c_hi * kPow;
     row.c_lo = c < 1e30 ? (float)(c - (double)row.c_hi) : 0.f;
@@ -645,47 +672,57 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     row.bits = a.bits;
     row.pow2 = sh.pow2;
     const double one = (double)(1ull << a.bits);
-    const double low = mp > 0.f ? log((double)mp) * (double)T : -INFINITY;  // min-p, as a bound on z - m
-    const float least = mp > 0.f ? fminf(__double2float_ru(row.dm + low), row.m) : -INFINITY;
+    const float least = mp > 0.f ? fminf(__double2float_ru(row.dm + sh.low), row.m) : -INFINITY;
     auto min_p_keeps = [&](float x) { return x >= least; };
     const float u = __ldg(a.u + r);
     // u outside [0, 1) is taken as its nearer end (at 1: the last token with weight)
     const double uu = fmin(u > 0.f ? (double)u : 0.0, 1.0 - 0x1p-50);
     auto logprob_of = [&](float x, double W) {
-        return (float)((x == row.m ? 0.0 : ((double)x - row.dm) * row.it) - log(W / one));
+        return (x == row.m ? 0.f : (float)(((double)x - row.dm) * row.it)) - logf((float)(W / one));
     };
     // at u below the resolution, the first kept token of any weight at all
     auto any_weight = [&](float x) { return x == row.m || ((double)x - row.dm) * row.it > -745.0; };
 
     // The first CTA's end of a row whose tokens of interest (n of them) are all in its list.
     auto draw_from_list = [&](int n, double target) {
-        const u64 v = t.sort(t.tid < n ? sh.list[t.tid] : 0ull, n);
-        const float x = logit_of((unsigned)(v >> 32));
-        const unsigned index = ~(unsigned)v;
-        const u64 w = t.tid < n ? row.weight(x) : 0ull;
-        const u64 upto = t.inclusive(w);
-        bool in = t.tid < n && (!need_k || t.tid < k);
-        if (need_k && need_p) target = (double)p * (double)t.block_sum(in ? w : 0ull);
-        in = in && (!need_p || t.tid == 0 || (double)(upto - w) < target) && min_p_keeps(x);
-        // in index order
-        __syncthreads();
-        sh.list[t.tid] = w;  // by rank
+        const u64 mine = t.tid < n ? sh.list[t.tid] : 0ull;
+        const int at = t.rank_of(mine, n);
         if (t.tid == 0) sh.token = 0xffffffffu;
-        const int kept = __syncthreads_count(in);
-        u64 o = t.sort(in ? ((u64)~index << 32 | (unsigned)t.tid) : 0ull, n);
-        const unsigned rank = (unsigned)o & (kList - 1);
-        const bool on = t.tid < kept;
-        const u64 w2 = on ? sh.list[rank] : 0ull, run = t.inclusive(w2);
-        const u64 W = t.block_sum(w2);
+        if (t.tid < n) sh.swap[at] = mine;
+        __syncthreads();
+        // in the order of the logits
+        const u64 v = t.tid < n ? sh.swap[t.tid] : 0ull;
+        const float x = logit_of((unsigned)(v >> 32));
+        const u64 w = t.tid < n ? row.weight(x) : 0ull;
+        bool in = t.tid < n && (!need_k || t.tid < k);
+        const u64 upto = t.inclusive(in ? w : 0ull);
+        if (need_k && need_p) {
+            if (t.tid == min(n, k) - 1) sh.pick[0] = upto;
+            __syncthreads();
+            target = (double)p * (double)sh.pick[0];
+        }
+        in = in && (!need_p || t.tid == 0 || (double)(upto - w) < target) && min_p_keeps(x);
+        const int kept = __syncthreads_count(in);  // the first `kept` tokens
+        if (t.tid == kept - 1) sh.pick[1] = upto;
+        // in the order of the indexes: the low words are ~index, so smaller is later
+        if (t.tid < kept) sh.list[t.tid] = (u64)(unsigned)v;
+        __syncthreads();
+        const u64 W = sh.pick[1];
+        const int place = t.rank_of((unsigned)v, kept);
+        if (t.tid < kept) sh.swap[place] = w;
+        __syncthreads();
         const double goal = uu * (double)W;
-        sh.swap[t.tid] = (u64)__float_as_uint(x);  // by rank (the sums' barriers came after the sort)
+        const u64 run = t.inclusive(t.tid < kept ? sh.swap[t.tid] : 0ull);
+        // the place where the running sum passes the goal; u below the resolution: the first token
+        // of any weight
+        if (t.tid < kept) {
+            if (goal < 1.0 ? false : (double)run > goal) atomicMin(&sh.token, (unsigned)t.tid);
+            if (goal < 1.0 && any_weight(x)) atomicMin(&sh.token, (unsigned)place);
+        }
         __syncthreads();
-        const float y = __uint_as_float((unsigned)sh.swap[rank]);
-        if (on && (goal < 1.0 ? any_weight(y) : (double)run > goal)) atomicMin(&sh.token, (unsigned)t.tid);
-        __syncthreads();
-        if ((unsigned)t.tid == sh.token) {
-            a.token[r] = (int)~(unsigned)(o >> 32);
-            if (a.logprob) a.logprob[r] = logprob_of(y, (double)W);
+        if (t.tid < kept && (unsigned)place == sh.token) {
+            a.token[r] = (int)~(unsigned)v;
+            if (a.logprob) a.logprob[r] = logprob_of(x, (double)W);
         }
     };
 
@@ -708,9 +745,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
     if (few_k) {
         const float from = bound <= 0x007fu ? -INFINITY : logit_of(bound << 16);
-        const unsigned n = t.gather(collect([&](float x) { return x >= from; }), v0);
-        if (n <= kList) {
-            if (t.rank == 0) draw_from_list((int)n, 0.0);
+        int n;
+        if (t.gather(collect([&](float x) { return x >= from; }), v0, 0, n)) {
+            if (t.rank == 0) draw_from_list(n, 0.0);
             return;
         }
     }
@@ -734,25 +771,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         double target = (double)k;
         const int b0 = t.find_bin(0, !need_k, mass0, need_k ? 0.0 : (double)p, target, bc, bm, oc, om);
         const bool whole = bc + oc <= kList;  // all tokens down to the border's bin fit the list
+        bool listed_all = false;
         if (mass0 && (whole || oc <= kList)) {
             // a first test that is cheaper than the bin: half a bin and the rounding below it
             const float from = b0 == kBins - 1 ? -INFINITY
                                                : (float)(row.dm - (b0 + 0.51 + 1e-5 * b0) / (double)row.scale0 - 1e-6 * fabs(row.dm));
-            const unsigned n = t.gather(collect([&](float x) {
+            int n;
+            listed_all = t.gather(collect([&](float x) {
                 if (!(x >= from)) return false;
                 const int b = row.bin0(x);
                 return b == b0 || (whole && b < b0);
-            }), v0);
-            if (whole) {
-                if (t.rank == 0) draw_from_list((int)n, target);
+            }), v0, 1, n);
+            if (listed_all && whole) {
+                if (t.rank == 0) draw_from_list(n, target);
                 return;
             }
             // -------- the last token kept, of the border's bin, to all CTAs
-            if (t.rank == 0) {
-                const u64 v = t.sort(t.tid < (int)n ? sh.list[t.tid] : 0ull, (int)n);
-                const u64 w = t.tid < (int)n ? row.weight(logit_of((unsigned)(v >> 32))) : 0ull;
+            if (listed_all && t.rank == 0) {
+                const u64 mine = t.tid < n ? sh.list[t.tid] : 0ull;
+                const int at = t.rank_of(mine, n);
+                if (t.tid < n) sh.swap[at] = mine;
+                __syncthreads();
+                const u64 v = t.tid < n ? sh.swap[t.tid] : 0ull;
+                const u64 w = t.tid < n ? row.weight(logit_of((unsigned)(v >> 32))) : 0ull;
                 const u64 ahead = bm + t.inclusive(w) - w;
-                const int in = __syncthreads_count(t.tid < (int)n && (bc + t.tid == 0 || (double)ahead < target));
+                const int in = __syncthreads_count(t.tid < n && (bc + t.tid == 0 || (double)ahead < target));
                 if (t.tid == in - 1)
                     for (unsigned i = 0; i < size; ++i) {
                         const uint32_t d = peer(&sh.pick[5], i);
@@ -760,11 +803,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                         peer_st(d + 4, ~(unsigned)v);
                     }
             }
-            cluster_sync();
-            bd.kt = (unsigned)sh.pick[5];
-            bd.c = 1;
-            last_equal = (int)(sh.pick[5] >> 32);
-        } else {
+            if (listed_all) {
+                cluster_sync();
+                bd.kt = (unsigned)sh.pick[5];
+                bd.c = 1;
+                last_equal = (int)(sh.pick[5] >> 32);
+            }
+        }
+        if (!listed_all) {
             // -------- many tokens in the border's bin, or a large k
             if (need_k && need_p) {  // now with the weights
                 cluster_sync();

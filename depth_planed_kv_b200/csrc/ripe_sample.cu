@@ -100,7 +100,6 @@ struct Shared {
     unsigned listed, token;
     unsigned count[2][kMaxCluster];  // tokens each CTA lists
     double it, c, low;               // the row's settings, see Row
-    int lo16;
 };
 
 __device__ __forceinline__ unsigned cluster_size() {
@@ -525,10 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const int r = blockIdx.x / size;
     Cta<Elem, RES> t{a, sh, reinterpret_cast<float*>(smem + sizeof(Shared)), nullptr, 0, cluster_rank(), size,
                      (int)threadIdx.x, (int)threadIdx.x / 32, (int)threadIdx.x % 32};
-    if (t.tid == 0) {
-        sh.listed = 0;
-        sh.lo16 = 0xffff;
-    }
+    if (t.tid == 0) sh.listed = 0;
     cluster_arrive();  // waited for before the first word to another CTA: by then all have started
     const int v0 = t.rank * a.per;
     t.z = reinterpret_cast<const Elem*>(a.z) + r * a.row_stride + v0;
@@ -619,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const bool need_k = k > 0 && k < a.V, need_p = p < 1.f, few_k = need_k && k <= kList * 3 / 4;
     unsigned bound = 0;
     if (few_k) {
-        const unsigned least16 = __reduce_min_sync(0xffffffffu, top >> 16);
-        if (t.lane == 0) atomicMin(&sh.lo16, (int)least16);
+        reinterpret_cast<unsigned short*>(sh.mine)[t.tid] = (unsigned short)(top >> 16);
+        __syncthreads();
     }
     {
         mx = sh.wmax[t.lane & (kWarps - 1)];
@@ -633,19 +629,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
     }
     if (few_k) {
-        const int want = (k + (int)size - 1) / (int)size;
-        __syncthreads();
-        unsigned lo = sh.lo16, hi = (key_of(mx) >> 16) + 1;  // all of the threads' maxima reach lo, none reaches hi
-        if (want > kThreads) hi = lo + 1;
-        while (hi - lo > 1) {
-            const unsigned mid = (lo + hi) / 2;
-            if (__syncthreads_count((top >> 16) >= mid) >= want) lo = mid; else hi = mid;
+        // one warp looks for the bound: 16 maxima a lane, in eight words
+        if (t.warp == 0) {
+            const int want = (k + (int)size - 1) / (int)size;
+            unsigned v[8], least16 = 0xffffu;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = sh.mine[t.lane + 32 * i];
+                least16 = min(least16, min(v[i] & 0xffffu, v[i] >> 16));
+            }
+            // all of the threads' maxima reach lo, none reaches hi
+            unsigned lo = __reduce_min_sync(0xffffffffu, least16), hi = (key_of(mx) >> 16) + 1;
+            if (want > kThreads) hi = lo + 1;
+            while (hi - lo > 1) {
+                const unsigned mid = (lo + hi) / 2;
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c += ((v[i] & 0xffffu) >= mid) + ((v[i] >> 16) >= mid);
+                if (__reduce_add_sync(0xffffffffu, c) >= want) lo = mid; else hi = mid;
+            }
+            bound = lo;  // t.tid < size tells the others
         }
-        bound = lo;
     }
     cluster_wait();
     {
         const Msg* g = t.exchange(bound, mx, mi);
+        bound = 0xffffu;
         for (unsigned i = 0; i < size; ++i) {
             better(g[i].mx, g[i].idx);
             bound = min(bound, (unsigned)g[i].sum);

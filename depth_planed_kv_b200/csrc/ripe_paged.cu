@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
     constexpr int ES = sizeof(Elem);
     extern __shared__ __align__(16) char smem[];
     __shared__ float s_p[kRows][kKT + 1];
+    __shared__ PagedPlanHead s_plan;
     const int pitch = simt_pitch(a.d, ES), tile = kKT * pitch;
     char* sQ = smem;                 // [16] rows
     char* sKV = smem + kRows * pitch;  // [2 buffers][K, V][32] rows
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
 
     if (tid == 0) a.hdr[blockIdx.x].kind = 0;
     PagedPlan<kKT> plan;
-    plan.template begin<kSimtThreads>(a, *reinterpret_cast<PagedPlanSmem*>(smem), kSimtMinCost);
+    plan.template begin<kSimtThreads>(a, s_plan, *reinterpret_cast<PagedPlanSmem*>(smem), kSimtMinCost);
     PagedSeg s;
     while (plan.next(a, s)) {
         const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1, rows = s.ntok * a.G;
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
             h.row0 = s.r + s.t0;
             h.ntok = s.ntok;
             h.head = s.head;
+            h.c0 = s.c0;
             a.hdr[blockIdx.x] = h;
         }
         if (!valid) continue;
@@ -264,8 +266,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
 // begin joins that item's partials, from the CTA that began it (its slot B) over the ones
 // in the middle to itself (slot A):
 //   m = max m_k, l = sum 2^(m_k - m) l_k, O = sum 2^(m_k - m) O_k / l.
-// A warp per row, its lanes over channel pairs.  Bound by L2 latency: the partials were
-// written just before.
+// A warp per row: lane k holds partial k's m and l (32 at a time), then the lanes take
+// channel pairs and the partials' loads go out together.  Bound by latency, three rounds
+// of L2 (the partials were written just before).
 constexpr int kMergeWarps = 4, kMergeThreads = 32 * kMergeWarps;
 
 template <typename Elem>
@@ -273,52 +276,67 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     grid_dependency_wait();
     const int c1 = blockIdx.x;
     const PagedHdr h = a.hdr[c1];
-    if (h.kind != 2) return;
-    int c0 = c1 - 1;
-    while (c0 > 0 && a.hdr[c0].kind == 1) --c0;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int stride = a.slot_rows * (a.d + 2);
+    const int i = blockIdx.y * kMergeWarps + warp;  // the item's row
+    if (h.kind != 2 || i >= h.ntok * a.G) return;
     // Rows of the item as its kernel numbered them: the tensor-memory kernel leaves the
     // rows of an M tile past its last token empty.
-    const int per = a.tok1 * a.G, gap = a.tpt > a.tok1 ? 128 - per : 0, rows = h.ntok * a.G;
-    for (int i = blockIdx.y * kMergeWarps + warp; i < rows; i += gridDim.y * kMergeWarps) {
-        const int row = i < per ? i : i + gap;
-        const float* first = paged_slot(a, c0, 1);
-        const float* rest = paged_slot(a, c0 + 1, 0);
-        const int n = c1 - c0;  // partials after the first
-        float m = first[row];
-        for (int k = lane; k < n; k += 32) m = fmaxf(m, rest[(int64_t)k * 2 * stride + row]);
+    const int per = a.tok1 * a.G, row = a.tpt > a.tok1 && i >= per ? i + 128 - per : i;
+    const int64_t stride = 2 * (int64_t)a.slot_rows * (a.d + 2);
+    // partial k: slot B of CTA c0, then slot A of c0 + 1 ... c1
+    const float* first = paged_slot(a, h.c0, 1);
+    const float* rest = paged_slot(a, h.c0, 0);
+    const int n = c1 - h.c0 + 1, np = a.d / 2;
+    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        const int k = k0 + lane;
+        float mk = -INFINITY, lk = 0.f;
+        if (k < n) {
+            const float* p = k == 0 ? first : rest + k * stride;
+            mk = p[row];
+            lk = p[a.slot_rows + row];
+        }
+        float mn = mk;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        const int np = a.d / 2;
-        for (int k = 0; k <= n; ++k) {
-            const float* p = k == 0 ? first : rest + (int64_t)(k - 1) * 2 * stride;
-            const float mk = p[row], f = mk == m ? 1.f : exp2f(mk - m);
-            l += f * p[a.slot_rows + row];
-            const float2* v = reinterpret_cast<const float2*>(p + 2 * a.slot_rows + row * a.d);
+        for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+        mn = fmaxf(mn, m);
+        const float f = m == mn ? 1.f : exp2f(m - mn), fk = mk == mn ? 1.f : exp2f(mk - mn);
+        m = mn;
+        l *= f;
+        float ls = fk * lk;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+        l += ls;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] *= f;
+        const int kn = min(32, n - k0);
+#pragma unroll 4
+        for (int q = 0; q < kn; ++q) {
+            const float* p = k0 + q == 0 ? first : rest + (k0 + q) * stride;
+            const float w = __shfl_sync(0xffffffffu, fk, q);
+            const float2* v = reinterpret_cast<const float2*>(p + 2 * a.slot_rows + (int64_t)row * a.d);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 if (lane + 32 * j < np) {
                     const float2 x = v[lane + 32 * j];
-                    o[2 * j] += f * x.x;
-                    o[2 * j + 1] += f * x.y;
+                    o[2 * j] += w * x.x;
+                    o[2 * j + 1] += w * x.y;
                 }
         }
-        const int tok = i / a.G, head = h.head * a.G + i - tok * a.G;
-        const int64_t orow = h.row0 + tok;
-        if (lane == 0 && a.lse) a.lse[orow * a.H + head] = m * 0.693147180559945309f + logf(l);
-        const float inv = 1.f / l;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (lane + 32 * j < np) {
-                char* dst = a.o + (orow * a.o_rs + (int64_t)head * a.d + 2 * (lane + 32 * j)) * sizeof(Elem);
-                if constexpr (sizeof(Elem) == 4)
-                    *reinterpret_cast<float2*>(dst) = make_float2(o[2 * j] * inv, o[2 * j + 1] * inv);
-                else
-                    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[2 * j] * inv, o[2 * j + 1] * inv);
-            }
     }
+    const int tok = i / a.G, head = h.head * a.G + i - tok * a.G;
+    const int64_t orow = h.row0 + tok;
+    if (lane == 0 && a.lse) a.lse[orow * a.H + head] = m * 0.693147180559945309f + logf(l);
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (lane + 32 * j < np) {
+            char* dst = a.o + (orow * a.o_rs + (int64_t)head * a.d + 2 * (lane + 32 * j)) * sizeof(Elem);
+            if constexpr (sizeof(Elem) == 4)
+                *reinterpret_cast<float2*>(dst) = make_float2(o[2 * j] * inv, o[2 * j + 1] * inv);
+            else
+                *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[2 * j] * inv, o[2 * j + 1] * inv);
+        }
 }
 
 template <typename Elem>
@@ -344,8 +362,7 @@ cudaError_t launch_paged_simt(PagedArgs a, int dtype, int grid, cudaStream_t st)
 
 cudaError_t launch_paged_merge(const PagedArgs& a, int dtype, int grid, cudaStream_t st) {
     const int most = a.tpt < a.max_ntok ? a.tpt : a.max_ntok;
-    int y = (most * a.G + kMergeWarps - 1) / kMergeWarps;
-    y = y < 1 ? 1 : y > 16 ? 16 : y;
+    const int y = (most * a.G + kMergeWarps - 1) / kMergeWarps;  // at most 64
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

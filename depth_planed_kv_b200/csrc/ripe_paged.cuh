@@ -25,7 +25,7 @@ constexpr int kPagedMaxSeqs = 1024;
 // What a CTA left in its slot A: 0 nothing, 1 a middle stretch of an item, 2 the end
 // of an item (then the item follows).
 struct PagedHdr {
-    int kind, row0, ntok, head, pad[4];
+    int kind, row0, ntok, head, c0, pad[3];  // c0: the CTA that began the item
 };
 
 struct PagedArgs {
@@ -129,16 +129,21 @@ struct PagedSeg {
     int seq, c, r, n;       // the sequence (PagedSeq)
     int t0, ntok, head, w;  // the row tile's tokens, the key/value head, M tiles
     int ta, tb;
+    int c0;                 // the CTA that began the item, for a stretch that does not
     PagedTiles tiles;
 };
 
+// What the plan needs of shared memory: a little of its own, and arrays for calls with many
+// row tiles, which may lie where copies land later.
+struct PagedPlanHead {
+    int64_t warp[32];
+    PagedSeg s;  // where the CTA's stretch begins, as one thread finds it
+    int qt, off;
+};
 struct PagedPlanSmem {
     int64_t cp[kPagedMaxSeqs + 1];  // one head's cost before each sequence
     int64_t tp[1024 + 1];           // one head's cost before each thread's run of row tiles
     int sq[kPagedMaxSeqs + 1];      // row tiles before each sequence
-    int64_t warp[32];
-    PagedSeg s;                     // where the CTA's stretch begins, as one thread finds it
-    int qt, off;
 };
 
 // Inclusive block-wide scan of one value per thread (all threads call it; one barrier).
@@ -170,6 +175,7 @@ __device__ __forceinline__ int64_t paged_div(int64_t a, int64_t b) {
 template <int KT>
 struct PagedPlan {
     int64_t x, x_end;  // this CTA's stretch of the line (x moves)
+    int64_t stretch;   // its length, before the line's end cuts it
     int qt;            // row tile within the sequence
     int off;           // cost already behind x within the item
     PagedSeg s;        // the current item (s.head included)
@@ -193,6 +199,8 @@ struct PagedPlan {
         const int64_t total = one_head * a.Hkv;
         int64_t len = paged_div(total + gridDim.x - 1, gridDim.x);
         len = len < min_cost ? min_cost : len;
+        s.c0 = 0;
+        stretch = len;
         x = len * blockIdx.x;
         x_end = x + len < total ? x + len : total;
     }
@@ -214,9 +222,19 @@ struct PagedPlan {
         off = (int)(y - p);
     }
 
-    // All threads of the block; `sm` may be reused after the call (it ends with a barrier).
+    // The thread that found the CTA's place tells the others.
+    __device__ __forceinline__ void tell(PagedPlanHead& h) {
+        // The item begins where its first key tile's cost ends up: a CTA that ends inside that
+        // tile leaves it to the next.
+        s.c0 = (int)paged_div(x - off + s.w - 1, stretch);
+        h.s = s;
+        h.qt = qt;
+        h.off = off;
+    }
+
+    // All threads of the block; ends with a barrier, after which `sm` may be reused.
     template <int THREADS>
-    __device__ void begin(const PagedArgs& a, PagedPlanSmem& sm, int min_cost) {
+    __device__ void begin(const PagedArgs& a, PagedPlanHead& h, PagedPlanSmem& sm, int min_cost) {
         static_assert(THREADS <= 1024, "one scan value per warp");
         const int tid = threadIdx.x;
         if (a.nseq <= THREADS && a.max_ntok <= 4 * a.tpt) {
@@ -232,15 +250,13 @@ struct PagedPlan {
                 for (qt = 0; qt * a.tpt < s.n; ++qt) cost += item(a);
             }
             int64_t total;
-            const int64_t incl = paged_scan<THREADS>(cost, sm.warp, total);
+            const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
             share(a, total, min_cost);
             if (x < x_end && (incl - cost) * a.Hkv <= x && x < incl * a.Hkv) {  // one thread's sequence
                 const int64_t y = head_of(a, incl - cost, cost);
                 qt = 0;
                 tile_of(a, 0, y);
-                sm.s = s;
-                sm.qt = qt;
-                sm.off = off;
+                tell(h);
             }
         } else {
             // row tiles before each sequence
@@ -249,7 +265,7 @@ struct PagedPlan {
                 const int i = i0 + tid;
                 int nq = 0, add;
                 if (i < a.nseq) nq = (paged_seq(a, i, blockIdx.x == 0).n + a.tpt - 1) / a.tpt;
-                const int incl = base + paged_scan<THREADS>(nq, reinterpret_cast<int*>(sm.warp), add);
+                const int incl = base + paged_scan<THREADS>(nq, reinterpret_cast<int*>(h.warp), add);
                 if (i < a.nseq) sm.sq[i + 1] = incl;
                 base += add;
                 __syncthreads();
@@ -267,7 +283,7 @@ struct PagedPlan {
                     step(a);
                 }
             }
-            const int64_t incl = paged_scan<THREADS>(cost, sm.warp, total);
+            const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
             sm.tp[tid] = incl - cost;
             __syncthreads();
             for (int i = tid; i <= a.nseq; i += THREADS) {
@@ -305,17 +321,14 @@ struct PagedPlan {
                     p = sm.cp[lo];
                 }
                 tile_of(a, p, y);
-                sm.s = s;
-                sm.qt = qt;
-                sm.off = off;
+                tell(h);
             }
         }
-        __syncthreads();
-        s = sm.s;
-        qt = sm.qt;
-        off = sm.off;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // asynchronous copies may land on `sm` next
         __syncthreads();
+        s = h.s;
+        qt = h.qt;
+        off = h.off;
     }
     // The sequence and row tile of global row tile q.
     __device__ __forceinline__ void find(const PagedArgs& a, const PagedPlanSmem& sm, int q) {

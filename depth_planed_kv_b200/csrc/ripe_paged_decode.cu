@@ -42,7 +42,8 @@ struct Lay {
     static constexpr int ML = BUF + kWarps * 8 * PITCH * 4;        // [warp][16] (m, l)
     static constexpr int BARS = ML + kWarps * 16 * 8;              // [warp][NS]
     static constexpr int MISC = BARS + kWarps * NS * 8;            // bad [warp], abort
-    static constexpr int TOTAL = MISC + 32;
+    static constexpr int PLAN = MISC + 32;
+    static constexpr int TOTAL = PLAN + (int)sizeof(PagedPlanHead);
     static_assert(sizeof(PagedPlanSmem) <= (size_t)BUF, "plan arrays over the stages");
     static_assert(TOTAL + 512 + 1024 <= 116736, "two CTAs per SM");
 };
@@ -71,26 +72,35 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         prefetch_tmap(&tm.v);
     }
     PagedPlan<kKT> plan;
-    plan.template begin<kThreads>(a, *reinterpret_cast<PagedPlanSmem*>(smem + L::STAGES), kMinCost);
+    plan.template begin<kThreads>(a, *reinterpret_cast<PagedPlanHead*>(smem + L::PLAN),
+                                  *reinterpret_cast<PagedPlanSmem*>(smem + L::STAGES), kMinCost);
 
     // ---- the warp's loads: its live blocks of all items in order, NS ahead
     PagedPlan<kKT> iplan = plan;
     PagedSeg is;
-    int it_t = 0, id = -1, issued = 0;
+    int it_t = 0, issued = 0, first = 0, ent = 0;  // ent: lane i, the table's entry for tile first + i of the item
     bool more = iplan.next(a, is);
-    // Moves to the next block with a key some row sees, and looks its page up.
+    // One load for 32 tiles' pages (a load per tile would hold each issue for its latency).
+    auto look_up = [&]() {
+        first = it_t;
+        const int t = it_t + lane, kb = is.tiles.tile(is.ta + t) * kKT + warp * 16;
+        ent = t < is.tb - is.ta && kb < is.c + is.t0 + is.ntok ? paged_entry(a, is.seq, kb) : 0;
+    };
+    if (more) look_up();
+    // Moves to the next block with a key some row sees.
     auto seek = [&]() {
         while (more) {
             while (it_t < is.tb - is.ta) {
                 const int kb = is.tiles.tile(is.ta + it_t) * kKT + warp * 16, p0 = is.c + is.t0;
                 if (paged_any_seen(a, kb, 16, p0, p0 + is.ntok - 1)) {
-                    id = paged_entry(a, is.seq, kb);
+                    if (it_t - first >= 32) look_up();
                     return;
                 }
                 ++it_t;
             }
             it_t = 0;
             more = iplan.next(a, is);
+            if (more) look_up();
         }
     };
     auto issue = [&]() {
@@ -98,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         const int st = issued % NS;
         char* dst = st_base + st * 2 * L::BLK;
         const int y = (is.tiles.tile(is.ta + it_t) * kKT + warp * 16) & (a.page - 1);
-        const int page = paged_checked(a, id);
+        const int page = paged_checked(a, __shfl_sync(0xffffffffu, ent, it_t - first));
         if (lane == 0) mbar_expect_tx(full + st, 2 * L::BLK);
         __syncwarp();
         if (lane < 2 * NCH)
@@ -279,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
             h.row0 = s.r + s.t0;
             h.ntok = s.ntok;
             h.head = s.head;
+            h.c0 = s.c0;
             a.hdr[blockIdx.x] = h;
         }
         float* part = paged_slot(a, blockIdx.x, slot);

@@ -59,6 +59,10 @@ struct Lay {
     static constexpr int SEG = ML + 2 * 128 * 8;  // the segments under way, as the TMA warp found them
     static constexpr int MISC = SEG + 2 * 64;
     static constexpr int TOTAL = MISC + 32;
+    // The plan is read before the first item, by the one warp that goes on with it; the joined
+    // (m, l) come after.
+    static constexpr int PLAN = ML;
+    static_assert(sizeof(PagedPlanHead) <= 2 * 128 * 8, "plan over (m, l)");
     static_assert(sizeof(PagedSeg) <= 64, "segment slots");
     static_assert(sizeof(PagedPlanSmem) <= (size_t)ST * TILE, "plan arrays over the stages");
     static_assert(ST >= 8, "the first products of an item need four key tiles, and its first values");
@@ -282,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     }
     if (warp == kTmaWarp && lane < 3) prefetch_tmap(lane == 0 ? &tm.q : lane == 1 ? &tm.k : &tm.v);
     PagedPlan<kKT> plan;  // carried on by the first TMA warp alone
-    plan.template begin<kThreads>(a, *reinterpret_cast<PagedPlanSmem*>(sKV), kMinCost);
+    plan.template begin<kThreads>(a, *reinterpret_cast<PagedPlanHead*>(smem + L::PLAN), *reinterpret_cast<PagedPlanSmem*>(sKV),
+                                  kMinCost);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -574,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 h.row0 = s.r + s.t0;
                 h.ntok = s.ntok;
                 h.head = s.head;
+                h.c0 = s.c0;
                 a.hdr[blockIdx.x] = h;
             }
             const bool two = s.w == 1 && T > 1;  // both streams hold a part of the one M tile

@@ -4,8 +4,8 @@
 // The keys and values are read once and each feeds at most 16 rows, so the bytes are
 // what counts: a row tile of 128 in the tensor-memory kernel would be 7/8 empty, and
 // its pipeline's hand-overs cost more than the loads.  Here each warp streams its own
-// 16 keys of every 64-key tile through its own ring of stages (one TMA box per 32
-// channels; the warp that waits is the one that reuses the stage, so there is no other
+// 16 keys of every 64-key tile through its own ring of stages (one TMA box for
+// the keys and one for the values; the warp that waits is the one that reuses the stage, so there is no other
 // hand-over) and keeps its own running maximum, sum and output in registers:
 //   S^T = K Q^T (keys on the 16-row side of m16n8k16, rows on its 8-column side),
 //   P^T by an 8x8 transpose in registers, O^T += V^T P^T.
@@ -111,9 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         const int page = paged_checked(a, __shfl_sync(0xffffffffu, ent, it_t - first));
         if (lane == 0) mbar_expect_tx(full + st, 2 * L::BLK);
         __syncwarp();
-        if (lane < 2 * NCH)
-            tma_load_4d(dst + lane * 1024, lane < NCH ? &tm.k : &tm.v, 32 * (lane < NCH ? lane : lane - NCH), y, is.head, page,
-                        full + st);
+        if (lane < 2) tma_load_5d(dst + lane * L::BLK, lane ? &tm.v : &tm.k, 0, y, 0, is.head, page, full + st);
         ++issued;
         ++it_t;
         seek();
@@ -388,6 +386,6 @@ cudaError_t launch_d(const DecodeMaps& tm, const PagedArgs& a, int grid, cudaStr
 
 cudaError_t launch_paged_decode(PagedArgs a, int grid, cudaStream_t st) {
     DecodeMaps tm;
-    if (!paged_kv_map(&tm.k, a.k, a, 16) || !paged_kv_map(&tm.v, a.v, a, 16)) return cudaErrorInvalidValue;
+    if (!paged_kv_map(&tm.k, a.k, a, 16, a.d / 32) || !paged_kv_map(&tm.v, a.v, a, 16, a.d / 32)) return cudaErrorInvalidValue;
     return a.slot_rows <= 8 ? launch_d<1>(tm, a, grid, st) : launch_d<2>(tm, a, grid, st);
 }

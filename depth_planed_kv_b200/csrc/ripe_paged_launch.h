@@ -6,9 +6,9 @@
 
 struct PagedArgs;
 
-// A tensor map of the pages at `base`: boxes of `rows` positions of one page and head,
-// 32 channels, 64-byte swizzle (false: the driver refused it).
-bool paged_kv_map(void* map, const void* base, const PagedArgs& a, int rows);
+// A tensor map of the pages at `base`: boxes of `rows` positions of one page and head and
+// `chunks` times 32 channels, 64-byte swizzle (false: the driver refused it).
+bool paged_kv_map(void* map, const void* base, const PagedArgs& a, int rows, int chunks);
 
 // The attention kernels: `grid` CTAs, partials for the merge kernel.
 cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st);

@@ -295,17 +295,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 
     if (warp >= kTmaWarp) {
         // ------------------------------------------------------------ TMA producers
-        // A tile is nsub (pages, or 64 keys of one) x NCH boxes, one per lane.  A lane's copy
-        // takes its warp about 70 cycles to issue, and a load another 250 for its barriers, so
-        // three warps take the loads in turn: with pages of 16 keys one warp alone brings 11
-        // bytes per cycle (HBM gives an SM 23).  Each waits for its own stages only; that
-        // cannot be off by a round, because stages are freed in the order of use and a warp
-        // comes round every kTmaWarps < ST loads.
+        // A tile is one box where a page holds it (64 keys), else nsub pages x NCH chunks of 32
+        // channels, a box per lane.  A lane's copy takes its warp about 70 cycles to issue, and a
+        // load another 250 for its barriers, so three warps take the loads in turn: with pages of
+        // 16 keys one warp alone brings 11 bytes per cycle (HBM gives an SM 23).  Each waits for
+        // its own stages only; that cannot be off by a round, because stages are freed in the
+        // order of use and a warp comes round every kTmaWarps < ST loads.
         static_assert(kTmaWarps < ST, "see above");
         const int pw = warp - kTmaWarp;
         const int pb = a.page < kKT ? a.page : kKT, nsub = kKT / pb;
-        const int sub = lane / NCH, ch = lane % NCH;
-        const uint32_t box = (uint32_t)pb * 64;
+        const int nch = nsub == 1 ? 1 : NCH;  // boxes of a page
+        const int sub = lane / nch, ch = lane % nch;
+        const uint32_t box = (uint32_t)pb * 64;  // bytes of a chunk of a page
         char* dst = sKV + ch * 4096 + sub * (int)box;
         int st = 0, ph = 1, turn = 0, n = 0;  // stage, its empty parity (the first round passes), whose load, segments begun
         bool ok = true;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     if (!warp_wait(kv_empty + st, ph, abort_flag, a.err)) return false;
                     if (lane == 0) mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
                     __syncwarp();
-                    if (on(t)) tma_load_4d(dst + st * L::TILE, map, 32 * ch, y, head, paged_checked(a, id), kv_full + st);
+                    if (on(t)) tma_load_5d(dst + st * L::TILE, map, 0, y, ch, head, paged_checked(a, id), kv_full + st);
                     __syncwarp();
                 }
                 if (++turn == kTmaWarps) turn = 0;
@@ -515,19 +516,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         if (threadIdx.x == 0) a.hdr[blockIdx.x].kind = 0;
         bool ok = true;
         while (ok && (ok = warp_wait(seg_full + (seg & 1), (seg >> 1) & 1, abort_flag, a.err))) {
-            const PagedSeg s = *s_seg[seg & 1];  // in registers: the loop below must not wait for loads
-            const int T = s.tb - s.ta;
+            const PagedSeg& s = *s_seg[seg & 1];
+            // what the loop over key tiles uses, in registers: it must not wait for loads
+            const int ta = s.ta, T = s.tb - ta, sw = s.w, ts = s.tiles.ts, skip = s.tiles.tlo - ts;
             if (T == 0) break;
-            const int ahead = s.w == 2 ? 2 : 4;
-            const int mytok = s.t0 + (s.w == 2 ? wg * a.tok1 : 0) + tok;  // this row's token
+            const int ahead = sw == 2 ? 2 : 4;
+            const int mytok = s.t0 + (sw == 2 ? wg * a.tok1 : 0) + tok;  // this row's token
             const bool valid = tok < a.tok1 && mytok < s.t0 + s.ntok;
             const int pos = s.c + mytok;
             const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1;
-            const int nsteps = s.w == 2 ? T : (T + 1 - wg) / 2;
+            const int nsteps = sw == 2 ? T : (T + 1 - wg) / 2;
             float m = -INFINITY, l = 0.f;
             // paged_all_seen of a tile in three comparisons
             const int full_hi = p0 - (kKT - 1), full_lo = a.window > 0 ? p1 - a.window : -1, full_first = a.sinks - kKT;
-            int tile = s.ta + (s.w == 2 ? 0 : wg);
+            int tile = ta + (sw == 2 ? 0 : wg);
             float x[32], y[32];
             auto scores = [&](uint32_t step) -> bool {  // waits for the stream's S of `step` and begins to load it
                 const uint32_t b = step & 1;
@@ -538,15 +540,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 return true;
             };
             if (nsteps > 0) ok = scores(steps);
-            for (int n = 0; n < nsteps && ok; ++n, ++steps, tile += s.w == 2 ? 1 : 2) {
-                const int k0 = (tile < s.tiles.ts ? tile : tile - s.tiles.ts + s.tiles.tlo) * kKT;
+            for (int n = 0; n < nsteps && ok; ++n, ++steps, tile += sw == 2 ? 1 : 2) {
+                const int k0 = (tile < ts ? tile : tile + skip) * kKT;
                 const bool part = k0 > full_hi || (k0 <= full_lo && k0 > full_first);
                 const uint32_t b = steps & 1;
                 if (part) {
                     // The tile's values, in the order the TMA warps load.  Only once the scores are
                     // there: their product was issued when every load up to `ahead` tiles back had
                     // arrived, so the parity cannot be that of the stage's earlier round.
-                    const int i = tile - s.ta, k = base + min(T, ahead) + i + min(i, max(T - ahead, 0)), st = k % ST;
+                    const int i = tile - ta, k = base + min(T, ahead) + i + min(i, max(T - ahead, 0)), st = k % ST;
                     if (!(ok = warp_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
                     if (clean_values<NCH>(sKV + st * L::TILE, t, p1 + 1 - k0)) {
                         s_bad[seg & 3] = seg + 1;
@@ -613,6 +615,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     a.lse[row * a.H + head] = (m + log2f(l)) * 0.693147180559945309f;
                 }
                 const float inv = whole ? 1.f / l : 1.f;
+                // where the rows of this lane's four go (0: nowhere), at this lane's piece
+                const uint64_t dst = !valid ? 0
+                                     : whole ? (uint64_t)(a.o + (row * a.o_rs + (int64_t)head * D) * 2)
+                                             : (uint64_t)(part + 2 * a.slot_rows + (int64_t)prow * D);
+                auto store = [&](uint4 (&v)[4], int at) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (dst) *reinterpret_cast<uint4*>(dst + at + k * 16) = v[k];
+                };
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
@@ -632,20 +643,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         mbar_arrive(o_free + wg);
                         if (two) mbar_arrive(o_free + 1);
                     }
-                    if (valid && whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.o + (row * a.o_rs + (int64_t)head * D + c) * 2);
+                    uint4 v[4];
+                    if (whole) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 8)
-                            dst[j / 8] = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
-                                                    pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
-                    } else if (valid) {
-                        float4* dst = reinterpret_cast<float4*>(part + 2 * a.slot_rows + (int64_t)prow * D + c);
+                            v[j / 8] = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
+                                                  pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
+                        store(v, 2 * c);
+                    } else {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        for (int q = 0; q < 32; q += 16) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                v[j / 4] = make_uint4(__float_as_uint(o[q + j]), __float_as_uint(o[q + j + 1]),
+                                                      __float_as_uint(o[q + j + 2]), __float_as_uint(o[q + j + 3]));
+                            store(v, 4 * (c + q));
+                        }
                     }
                     __syncwarp();
                 }
-                if (bad && valid) {  // onto what this thread has just written
+                if (bad && valid) {  // onto what the warp has just written
                     for (int c = 0; c < D; ++c) {
                         const float x = paged_nonfinite<kKT>(a, s, pos, c);
                         if (x == 0.f) continue;
@@ -700,15 +717,16 @@ cudaError_t launch(const PagedMaps& tm, const PagedArgs& a, int grid, cudaStream
 }  // namespace
 
 // Maps of the pages ([pages][heads][positions][d], any strides) in boxes of `rows`
-// positions of one page and head and 32 channels.
-bool paged_kv_map(void* map, const void* base, const PagedArgs& a, int rows) {
+// positions of one page and head and `chunks` times 32 channels, which land one chunk
+// behind the other.
+bool paged_kv_map(void* map, const void* base, const PagedArgs& a, int rows, int chunks) {
     const auto encode = encode_fn();
     if (!encode) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)a.d, (cuuint64_t)a.page, (cuuint64_t)a.Hkv, (cuuint64_t)a.npages};
-    const cuuint64_t strides[3] = {(cuuint64_t)a.pos_stride * 2, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
-    const cuuint32_t box[4] = {32, (cuuint32_t)rows, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return encode(reinterpret_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+    const cuuint64_t dims[5] = {32, (cuuint64_t)a.page, (cuuint64_t)a.d / 32, (cuuint64_t)a.Hkv, (cuuint64_t)a.npages};
+    const cuuint64_t strides[4] = {(cuuint64_t)a.pos_stride * 2, 64, (cuuint64_t)a.head_stride * 2, (cuuint64_t)a.page_stride * 2};
+    const cuuint32_t box[5] = {32, (cuuint32_t)rows, (cuuint32_t)chunks, 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return encode(reinterpret_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -727,8 +745,8 @@ cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st) {
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const int rows = a.page < kKT ? a.page : kKT;
-    if (!paged_kv_map(&tm.k, a.k, a, rows) || !paged_kv_map(&tm.v, a.v, a, rows)) return cudaErrorInvalidValue;
+    const int rows = a.page < kKT ? a.page : kKT, chunks = rows == kKT ? a.d / 32 : 1;
+    if (!paged_kv_map(&tm.k, a.k, a, rows, chunks) || !paged_kv_map(&tm.v, a.v, a, rows, chunks)) return cudaErrorInvalidValue;
     if (a.d == 64) return launch<64, 22>(tm, a, grid, st);
     if (a.d == 96) return launch<96, 14>(tm, a, grid, st);
     if (a.d == 128) return launch<128, 10>(tm, a, grid, st);

@@ -3,6 +3,8 @@
 // the tensor-core kernels have no form for, and the kernel that joins cut items.
 #include <math.h>
 
+#include <type_traits>
+
 #include "ripe_launch.h"
 #include "ripe_paged.cuh"
 #include "ripe_paged_launch.h"
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // shared memory by cp.async as they lie in the cache; fp32 arithmetic (FFMA).  Eight
 // lanes share a row: four of the 32 scores each, then d/8 channels of O each.
 constexpr int kSimtThreads = 128, kRows = 16, kKT = 32;
-constexpr int kSimtMinCost = 4;
+constexpr int kSimtMinCost = 2;
 
 template <typename Elem>
 __device__ __forceinline__ float4 load4(const char* p);
@@ -137,17 +139,24 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                                        : 0),
                              on);
         }
+        // Four threads a key; its page is looked up a tile ahead of its copies.
+        const int lr = tid / 4, lv = tid % 4;
+        auto entry = [&](int t) {
+            const int key = s.tiles.tile(t) * kKT + lr;
+            return t < s.tb && key <= p1 ? paged_entry(a, s.seq, key) : 0;
+        };
+        int ent = entry(s.ta);
         auto load = [&](int t, int b) {
-            const int k0 = s.tiles.tile(t) * kKT;
-            char* dk = sKV + b * 2 * tile;
-            for (int i = tid; i < kKT * nv; i += kSimtThreads) {
-                const int r = i / nv, v = i - r * nv, key = k0 + r;
-                const bool on = key <= p1;  // later slots hold anything: read as zeros
-                const int64_t off = on ? (paged_page(a, s.seq, key) * a.page_stride + s.head * a.head_stride +
-                                          (key & (a.page - 1)) * a.pos_stride) * ES + v * 16
-                                       : 0;
-                cp_async16_zfill(dk + r * pitch + v * 16, a.k + off, on);
-                cp_async16_zfill(dk + tile + r * pitch + v * 16, a.v + off, on);
+            const int key = s.tiles.tile(t) * kKT + lr;
+            const bool on = key <= p1;  // later slots hold anything: read as zeros
+            const int64_t off = on ? (paged_checked(a, ent) * a.page_stride + s.head * a.head_stride +
+                                      (key & (a.page - 1)) * a.pos_stride) * ES
+                                   : 0;
+            ent = entry(t + 1);
+            char* dk = sKV + b * 2 * tile + lr * pitch;
+            for (int v = lv; v < nv; v += 4) {
+                cp_async16_zfill(dk + v * 16, a.k + off + (on ? v * 16 : 0), on);
+                cp_async16_zfill(dk + tile + v * 16, a.v + off + (on ? v * 16 : 0), on);
             }
             cp_async_commit();
         };
@@ -199,21 +208,28 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                 s_p[row][sub + 8 * j] = e;
             }
             __syncwarp();  // a row's eight lanes sit in one warp
-            auto add = [&](int key) {
+            auto add = [&](int key, auto partial) {
                 const float p = s_p[row][key];
-                if (part && p == 0.f) return;  // a hidden key's value may be anything
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (sub + 8 * j < n4) {
                         const float4 v = load4<Elem>(V + key * pitch + (sub + 8 * j) * 4 * ES);
-                        o[j].x = fmaf(p, v.x, o[j].x);
-                        o[j].y = fmaf(p, v.y, o[j].y);
-                        o[j].z = fmaf(p, v.z, o[j].z);
-                        o[j].w = fmaf(p, v.w, o[j].w);
+                        // a hidden key's value may be anything: it must not meet the zero weight
+                        const bool skip = partial.value && p == 0.f;
+                        o[j].x = skip ? o[j].x : fmaf(p, v.x, o[j].x);
+                        o[j].y = skip ? o[j].y : fmaf(p, v.y, o[j].y);
+                        o[j].z = skip ? o[j].z : fmaf(p, v.z, o[j].z);
+                        o[j].w = skip ? o[j].w : fmaf(p, v.w, o[j].w);
                     }
                 }
             };
-            for (int key = 0; key < kKT; ++key) add(key);
+            if (part) {
+#pragma unroll 8
+                for (int key = 0; key < kKT; ++key) add(key, std::true_type());
+            } else {
+#pragma unroll 8
+                for (int key = 0; key < kKT; ++key) add(key, std::false_type());
+            }
             __syncthreads();  // before the next load into this buffer
         }
 #pragma unroll

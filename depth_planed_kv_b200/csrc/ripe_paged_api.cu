@@ -79,12 +79,12 @@ int make_plan(const ripe_pages_t* p, int H, int max_ntok, Plan& q) {
     if (H < 1 || H > 256 || H % p->Hkv)
         return ripe_fail(RIPE_ERR_INVALID_ARG, "H=%d is not a multiple of Hkv=%d in [1,256]", H, p->Hkv);
     if (max_ntok < 1) return ripe_fail(RIPE_ERR_INVALID_ARG, "max_ntok=%d < 1", max_ntok);
-    const int sms = device_sm_count();
-    if (sms < 1) return ripe_fail(RIPE_ERR_CUDA, "no current CUDA device");
     q.G = H / p->Hkv;
     const bool tc = fused_supported(p->dtype, p->d);
     if (q.G > (tc ? 128 : 16))
         return ripe_fail(RIPE_ERR_UNSUPPORTED, "%d query heads per key/value head: at most %d here", q.G, tc ? 128 : 16);
+    const int sms = device_sm_count();
+    if (sms < 1) return ripe_fail(RIPE_ERR_CUDA, "no current CUDA device");
     if (tc && (int64_t)max_ntok * q.G <= 16) {
         q.kind = Plan::DECODE;
         q.grid = 2 * sms;
@@ -186,8 +186,9 @@ int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, 
     a.o_rs = o_stride;
     a.H = H;
     a.G = q.G;
-    a.window = window;
-    a.sinks = sinks;
+    constexpr int kMost = 1 << 30;  // positions are below it: differences stay within 32 bits
+    a.window = window < kMost ? window : kMost;
+    a.sinks = sinks < kMost ? sinks : kMost;
     a.max_ntok = batch->max_ntok;
     a.tok1 = q.tok1;
     a.tpt = q.tpt;

@@ -603,6 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             const bool two = s.w == 1 && T > 1;  // both streams hold a part of the one M tile
             if (two && wg == 1) {
+                // not before the other stream has read the join before: it then left this one's O
+                if (uses1 > 0 && !(ok = warp_wait(o_free + 1, (uses1 - 1) & 1, abort_flag, a.err))) break;
                 s_ml[(joins & 1) * 128 + t] = make_float2(m, l);
                 mbar_arrive(ml_full);
             }

@@ -424,7 +424,8 @@ typedef struct {
  * whose offsets are wrong (RIPE_DEVERR_ROWS) or whose tokens do not fit its
  * table_width*page <= 2^30 positions (RIPE_DEVERR_CAPACITY) is skipped: its rows are
  * left as they were, and so are rows that belong to no sequence.  err_dev (device int32,
- * or NULL) receives the first such condition, like a cache's device error word.
+ * or NULL) receives the first such condition, like a cache's device error word (a bounded
+ * wait that ran out, RIPE_DEVERR_TIMEOUT, included: that call's outputs are incomplete).
  */
 typedef struct {
     const int32_t* table;

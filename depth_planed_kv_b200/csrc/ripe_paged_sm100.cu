@@ -252,6 +252,13 @@ __device__ __forceinline__ bool softmax_step(float* x, float* y, uint32_t s_col,
     return true;
 }
 
+// Key tiles of a stretch that M tile 0 of two needs: those up to its own last token (the
+// rest are M tile 1's alone).
+__device__ __forceinline__ int first_tiles(const PagedArgs& a, const PagedSeg& s) {
+    const int end = (s.c + s.t0 + a.tok1 - 1) / kKT + 1 - (s.tiles.tlo - s.tiles.ts);
+    return max(0, min(s.tb, end) - s.ta);
+}
+
 template <int D, int ST>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedMaps tm,
                                                                const __grid_constant__ PagedArgs a) {
@@ -455,13 +462,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 const PagedSeg& s = *s_seg[seg & 1];
                 const int T = s.tb - s.ta;
                 const bool two = s.w == 2;
+                const int T0 = two ? first_tiles(a, s) : 0;
                 mbar_arrive(seg_empty + (seg & 1));
                 if (T == 0) break;
                 if (!(ok = mbar_wait_idle(q_full, seg & 1, abort_flag, a.err))) break;
                 ++seg;
                 if (two) {
                     for (int i = 0; i < 2 && i < T && (ok = stage()); ++i) {
-                        qk(s0, 0);
+                        if (i < T0) qk(s0, 0);
                         qk(s1, 1);
                         next_stage();
                     }
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     for (int i = 0; i < T && ok; ++i) {
                         if (!(ok = stage())) break;
                         const int vst = st;
-                        if (!(ok = pv(s0, i == 0, i + 1 == T))) break;
+                        if (i < T0 && !(ok = pv(s0, i == 0, i + 1 == T0))) break;
                         if (i + 2 < T) {
                             // the keys two tiles on lie in the next stage
                             const uint32_t vph = ph;
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             const int kst = st;
                             const uint32_t kph = ph;
                             if (!(ok = stage())) break;
-                            qk(s0, 0);
+                            if (i + 2 < T0) qk(s0, 0);
                             st = vst;
                             ph = vph;
                             if (!(ok = pv(s1, i == 0, false))) break;
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             const bool valid = tok < a.tok1 && mytok < s.t0 + s.ntok;
             const int pos = s.c + mytok;
             const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1;
-            const int nsteps = sw == 2 ? T : (T + 1 - wg) / 2;
+            const int nsteps = sw == 1 ? (T + 1 - wg) / 2 : wg ? T : first_tiles(a, s);
             float m = -INFINITY, l = 0.f;
             // paged_all_seen of a tile in three comparisons
             const int full_hi = p0 - (kKT - 1), full_lo = a.window > 0 ? p1 - a.window : -1, full_first = a.sinks - kKT;
@@ -610,7 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             if (s.w == 2 || wg == 0) {
                 float f0 = 1.f, f1 = 0.f;
-                if (!(ok = warp_wait(o_full + wg, uses & 1, abort_flag, a.err))) break;
+                const bool any = nsteps > 0;  // else these rows have nothing in this stretch
+                if (any && !(ok = warp_wait(o_full + wg, uses & 1, abort_flag, a.err))) break;
                 if (two) {
                     if (!(ok = warp_wait(ml_full, joins & 1, abort_flag, a.err))) break;
                     if (!(ok = warp_wait(o_full + 1, uses1 & 1, abort_flag, a.err))) break;
@@ -657,7 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     } else {
                         tmem_wait_ld32(o);
                     }
-                    if (c + 32 == D) {
+                    if (!any) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                    } else if (c + 32 == D) {
                         tc_fence_before();
                         mbar_arrive(o_free + wg);
                         if (two) mbar_arrive(o_free + 1);
@@ -692,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 }
             }
             uses1 += s.w == 2 || two;
-            uses = wg ? uses1 : uses + 1;
+            uses = wg ? uses1 : uses + (nsteps > 0);
             joins += two;
             base += 2 * T;
             __syncwarp();

@@ -121,6 +121,12 @@ __device__ __forceinline__ void hide(float* v, uint32_t see) {
     for (int j = 0; j < 32; ++j) v[j] = (see >> j) & 1 ? v[j] : -INFINITY;
 }
 
+// s + 0 * w, two bf16 each.
+__device__ __forceinline__ uint32_t zero_times(uint32_t w, uint32_t s) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(s));
+    return d;
+}
 // Zeros the values the matrix product must not see in a key tile that some row sees
 // only in part: keys from `end` (of the tile) on, whose slots hold anything, and values
 // that are not finite (returns whether there were any; paged_nonfinite puts them back
@@ -129,8 +135,23 @@ __device__ __forceinline__ void hide(float* v, uint32_t see) {
 // still writes is what the earlier one wrote.
 template <int NCH>
 __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
+    if (end >= kKT) {
+        // 0 * x adds up to 0 if x are all finite, else to NaN: an instruction a pair
+        uint4 x[NCH * 2];
+        uint32_t s0 = 0, s1 = 0;
+#pragma unroll
+        for (int i = 0; i < NCH * 2; ++i) x[i] = reinterpret_cast<const uint4*>(sv)[t + i * 128];
+#pragma unroll
+        for (int i = 0; i < NCH * 2; ++i) {
+            s0 = zero_times(x[i].x, s0);
+            s1 = zero_times(x[i].y, s1);
+            s0 = zero_times(x[i].z, s0);
+            s1 = zero_times(x[i].w, s1);
+        }
+        if ((s0 | s1) == 0) return false;
+    }
     bool found = false;
-#pragma unroll 4
+#pragma unroll 2
     for (int i = t; i < NCH * 256; i += 128) {
         uint4* at = reinterpret_cast<uint4*>(sv) + i;
         uint4 x = *at;

@@ -293,11 +293,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
     const int c1 = blockIdx.x;
     const PagedHdr h = a.hdr[c1];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int i = blockIdx.y * kMergeWarps + warp;  // the item's row
-    if (h.kind != 2 || i >= h.ntok * a.G) return;
-    // Rows of the item as its kernel numbered them: the tensor-memory kernel leaves the
-    // rows of an M tile past its last token empty.
-    const int per = a.tok1 * a.G, row = a.tpt > a.tok1 && i >= per ? i + 128 - per : i;
+    const int row = blockIdx.y * kMergeWarps + warp;  // the item's
+    if (h.kind != 2 || row >= h.ntok * a.G) return;
     const int64_t stride = 2 * (int64_t)a.slot_rows * (a.d + 2);
     // partial k: slot B of CTA c0, then slot A of c0 + 1 ... c1
     const float* first = paged_slot(a, h.c0, 1);
@@ -340,7 +337,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
                 }
         }
     }
-    const int tok = i / a.G, head = h.head * a.G + i - tok * a.G;
+    const int tok = row / a.G, head = h.head * a.G + row - tok * a.G;
     const int64_t orow = h.row0 + tok;
     if (lane == 0 && a.lse) a.lse[orow * a.H + head] = m * 0.693147180559945309f + logf(l);
     const float inv = 1.f / l;
@@ -378,19 +375,10 @@ cudaError_t launch_paged_simt(PagedArgs a, int dtype, int grid, cudaStream_t st)
 
 cudaError_t launch_paged_merge(const PagedArgs& a, int dtype, int grid, cudaStream_t st) {
     const int most = a.tpt < a.max_ntok ? a.tpt : a.max_ntok;
-    const int y = (most * a.G + kMergeWarps - 1) / kMergeWarps;  // at most 64
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)y);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = st;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    ripe_count_launch();
-    return dtype == RIPE_F32 ? cudaLaunchKernelEx(&cfg, paged_merge_kernel<float>, a)
-                             : cudaLaunchKernelEx(&cfg, paged_merge_kernel<__nv_bfloat16>, a);
+    const int y = (most * a.G + kMergeWarps - 1) / kMergeWarps;
+    const dim3 g((unsigned)grid, (unsigned)y);
+    return dtype == RIPE_F32 ? launch_paged_dependent(paged_merge_kernel<float>, g, kMergeThreads, st, a)
+                             : launch_paged_dependent(paged_merge_kernel<__nv_bfloat16>, g, kMergeThreads, st, a);
 }
 
 cudaError_t launch_paged_append(const PagedArgs& a, const char* K, const char* V, int64_t row_stride, int esize,

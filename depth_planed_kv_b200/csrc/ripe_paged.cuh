@@ -389,7 +389,24 @@ __device__ __forceinline__ bool paged_whole(const PagedSeg& s) { return s.ta == 
 __device__ __forceinline__ float* paged_slot(const PagedArgs& a, int cta, int slot) {
     return a.part + ((int64_t)cta * 2 + slot) * a.slot_rows * (a.d + 2);
 }
-// A slot holds m [slot_rows] (log2 units), l [slot_rows], then O [slot_rows][d].
+// A slot holds m [slot_rows] (log2 units), l [slot_rows], then O [slot_rows][d] (in the
+// tensor-memory kernel's own order).
+
+// Launches a kernel that begins beside the one before it and waits for its end.
+template <typename Kernel>
+cudaError_t launch_paged_dependent(Kernel kernel, dim3 grid, int threads, cudaStream_t st, const PagedArgs& a) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    ripe_count_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
 
 // The sum of the values of V in channel c that are not finite, of keys the row sees in
 // key tiles that are not seen whole by all rows (0 if there are none): the kernels read

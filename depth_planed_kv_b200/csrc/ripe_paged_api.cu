@@ -202,7 +202,7 @@ int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, 
     cudaError_t e = q.kind == Plan::DECODE ? launch_paged_decode(a, q.grid, st)
                     : q.kind == Plan::TC   ? launch_paged_tc(a, q.grid, st)
                                            : launch_paged_simt(a, pages->dtype, q.grid, st);
-    if (e == cudaSuccess) e = launch_paged_merge(a, pages->dtype, q.grid, st);
+    if (e == cudaSuccess && q.kind != Plan::TC) e = launch_paged_merge(a, pages->dtype, q.grid, st);
     return e == cudaSuccess ? RIPE_OK : ripe_fail(RIPE_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
 }
 

@@ -280,6 +280,15 @@ __device__ __forceinline__ int first_tiles(const PagedArgs& a, const PagedSeg& s
     return max(0, min(s.tb, end) - s.ta);
 }
 
+// Where O's channel c of row r lies in a slot: eight rows' pieces of 16 bytes side by side,
+// so that a warp's store, a piece of 32 rows, fills four lines rather than a sector in each
+// of 32 (the last item's end, of a CTA that leaves a partial, took 10000 cycles of 154000
+// for 2048 tokens of 55 heads).
+template <int D>
+__device__ __forceinline__ constexpr int slot_at(int r, int c) {
+    return ((r >> 3) * (D / 4) + (c >> 2)) * 32 + (r & 7) * 4 + (c & 3);
+}
+
 template <int D, int ST>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedMaps tm,
                                                                const __grid_constant__ PagedArgs a) {
@@ -664,14 +673,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     a.lse[row * a.H + head] = (m + log2f(l)) * 0.693147180559945309f;
                 }
                 const float inv = whole ? 1.f / l : 1.f;
-                // where the rows of this lane's four go (0: nowhere), at this lane's piece
+                // where this lane's row goes (0: nowhere)
                 const uint64_t dst = !valid ? 0
                                      : whole ? (uint64_t)(a.o + (row * a.o_rs + (int64_t)head * D) * 2)
-                                             : (uint64_t)(part + 2 * a.slot_rows + (int64_t)prow * D);
-                auto store = [&](uint4 (&v)[4], int at) {
+                                             : (uint64_t)(part + 2 * a.slot_rows + slot_at<D>(prow, 0));
+                auto store = [&](uint4 (&v)[4], int at, int step) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (dst) *reinterpret_cast<uint4*>(dst + at + k * 16) = v[k];
+                        if (dst) *reinterpret_cast<uint4*>(dst + at + k * step) = v[k];
                 };
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
@@ -701,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         for (int j = 0; j < 32; j += 8)
                             v[j / 8] = make_uint4(pack_bf16(o[j] * inv, o[j + 1] * inv), pack_bf16(o[j + 2] * inv, o[j + 3] * inv),
                                                   pack_bf16(o[j + 4] * inv, o[j + 5] * inv), pack_bf16(o[j + 6] * inv, o[j + 7] * inv));
-                        store(v, 2 * c);
+                        store(v, 2 * c, 16);
                     } else {
 #pragma unroll
                         for (int q = 0; q < 32; q += 16) {
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                             for (int j = 0; j < 16; j += 4)
                                 v[j / 4] = make_uint4(__float_as_uint(o[q + j]), __float_as_uint(o[q + j + 1]),
                                                       __float_as_uint(o[q + j + 2]), __float_as_uint(o[q + j + 3]));
-                            store(v, 4 * (c + q));
+                            store(v, 4 * slot_at<D>(0, c + q), 4 * slot_at<D>(0, 4));
                         }
                     }
                     __syncwarp();
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                         if (x == 0.f) continue;
                         __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(a.o) + row * a.o_rs + (int64_t)head * D + c;
                         if (whole) *at = __float2bfloat16_rn(__bfloat162float(*at) + x);
-                        else part[2 * a.slot_rows + (int64_t)prow * D + c] += x;
+                        else part[2 * a.slot_rows + slot_at<D>(prow, c)] += x;
                     }
                 }
             }
@@ -739,6 +748,58 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the partials of an item that was cut, as paged_merge_kernel does, from this
+// kernel's slots: a warp takes eight rows, four lanes a row, and carries on maximum, sum
+// and O from partial to partial (a partial's loads wait for nothing but the header).
+constexpr int kMergeWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_tc_merge_kernel(const __grid_constant__ PagedArgs a) {
+    grid_dependency_wait();
+    const int c1 = blockIdx.x;
+    const PagedHdr h = a.hdr[c1];
+    const int lane = threadIdx.x % 32, piece = lane / 8;
+    const int row = (blockIdx.y * kMergeWarps + threadIdx.x / 32) * 8 + lane % 8;  // of the slot
+    // the item's row: an M tile's rows past its last token are empty
+    const int per = a.tok1 * a.G, i = row < 128 ? row : row - 128 + per;
+    if (h.kind != 2 || (row & 127) >= per || i >= h.ntok * a.G) return;
+    const int64_t stride = 2 * (int64_t)a.slot_rows * (D + 2);
+    // partial k: slot B of CTA c0, then slot A of c0 + 1 ... c1
+    const float* first = paged_slot(a, h.c0, 1);
+    const float* rest = paged_slot(a, h.c0, 0);
+    const int n = c1 - h.c0 + 1;
+    float m = -INFINITY, l = 0.f;
+    float4 o[D / 16];
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < n; ++k) {
+        const float* p = k == 0 ? first : rest + k * stride;
+        const float mk = p[row], lk = p[a.slot_rows + row];
+        const float mn = fmaxf(m, mk);
+        const float f = m == mn ? 1.f : exp2f(m - mn), w = mk == mn ? 1.f : exp2f(mk - mn);
+        m = mn;
+        l = l * f + lk * w;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 2 * a.slot_rows + slot_at<D>(row, 16 * j + 4 * piece));
+            o[j].x = o[j].x * f + x.x * w;
+            o[j].y = o[j].y * f + x.y * w;
+            o[j].z = o[j].z * f + x.z * w;
+            o[j].w = o[j].w * f + x.w * w;
+        }
+    }
+    const int tok = i / a.G, head = h.head * a.G + i - tok * a.G;
+    const int64_t orow = h.row0 + tok;
+    if (piece == 0 && a.lse) a.lse[orow * a.H + head] = m * 0.693147180559945309f + logf(l);
+    const float inv = 1.f / l;
+    char* dst = a.o + (orow * a.o_rs + (int64_t)head * D + 4 * piece) * 2;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+        *reinterpret_cast<uint2*>(dst + 32 * j) =
+            make_uint2(pack_bf16(o[j].x * inv, o[j].y * inv), pack_bf16(o[j].z * inv, o[j].w * inv));
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -763,7 +824,12 @@ cudaError_t launch(const PagedMaps& tm, const PagedArgs& a, int grid, cudaStream
     if (e != cudaSuccess) return e;
     paged_tc_kernel<D, ST><<<grid, kThreads, smem, st>>>(tm, a);
     ripe_count_launch();
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // rows of the items: M tile 1 begins at slot row 128
+    const int most = a.max_ntok <= a.tok1 ? a.max_ntok * a.G : 128 + (min(a.max_ntok, a.tpt) - a.tok1) * a.G;
+    return launch_paged_dependent(paged_tc_merge_kernel<D>, dim3((unsigned)grid, (unsigned)((most + 8 * kMergeWarps - 1) / (8 * kMergeWarps))),
+                                  32 * kMergeWarps, st, a);
 }
 
 }  // namespace
@@ -782,8 +848,6 @@ bool paged_kv_map(void* map, const void* base, const PagedArgs& a, int rows, int
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-int paged_tc_slot_rows() { return 256; }
 
 cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st) {
     PagedMaps tm;

@@ -133,7 +133,7 @@ __device__ __forceinline__ uint32_t zero_times(uint32_t w, uint32_t s) {
 // where they are seen).  128 threads, 16 bytes at a time in the order they lie.  With two
 // M tiles both streams clean the tile, each before its own product: what the later one
 // still writes is what the earlier one wrote.
-template <int NCH>
+template <int NCH, bool GROUPS>
 __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
     if (end >= kKT) {
         // 0 * x adds up to 0 if x are all finite, else to NaN: an instruction a pair
@@ -155,7 +155,8 @@ __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
     for (int i = t; i < NCH * 256; i += 128) {
         uint4* at = reinterpret_cast<uint4*>(sv) + i;
         uint4 x = *at;
-        if (((i & 255) >> 2) >= end) {  // four 16-byte units a key
+        const int key = GROUPS ? i / (NCH * 32) * 8 + ((i & 31) >> 2) : (i & 255) >> 2;  // four 16-byte units a key and chunk
+        if (key >= end) {
             if (x.x | x.y | x.z | x.w) *at = make_uint4(0, 0, 0, 0);
             continue;
         }
@@ -289,7 +290,13 @@ __device__ __forceinline__ constexpr int slot_at(int r, int c) {
     return ((r >> 3) * (D / 4) + (c >> 2)) * 32 + (r & 7) * 4 + (c & 3);
 }
 
-template <int D, int ST>
+// A key tile lies in its stage as 32-channel chunks of 64 keys one behind the other, or, by
+// GROUPS, as groups of eight keys one behind the other, all chunks of a group together.  A
+// box brings what one page holds of that: all 64 keys and chunks, or one chunk of a smaller
+// page; by groups, eight keys of all chunks.  Groups are taken for pages of 16 keys: 8 boxes
+// a tile instead of 16 (12 for head size 96, 8 for 64), and boxes are what such pages cost
+// (64 draft blocks of 8 tokens, head size 128: 139 us with chunks, 130 with groups).
+template <int D, int ST, bool GROUPS>
 __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_constant__ PagedMaps tm,
                                                                const __grid_constant__ PagedArgs a) {
     using L = Lay<D, ST>;
@@ -357,11 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         // order of use and a warp comes round every kTmaWarps < ST loads.
         static_assert(kTmaWarps < ST, "see above");
         const int pw = warp - kTmaWarp;
-        const int pb = a.page < kKT ? a.page : kKT, nsub = kKT / pb;
-        const int nch = nsub == 1 ? 1 : NCH;  // boxes of a page
+        const int pb = GROUPS ? 8 : a.page < kKT ? a.page : kKT, nsub = kKT / pb;
+        const int nch = GROUPS || nsub == 1 ? 1 : NCH;  // boxes of pb keys
         const int sub = lane / nch, ch = lane % nch;
-        const uint32_t box = (uint32_t)pb * 64;  // bytes of a chunk of a page
-        char* dst = sKV + ch * 4096 + sub * (int)box;
+        const uint32_t box = (uint32_t)pb * 64;  // bytes of a chunk of pb keys
+        char* dst = sKV + (GROUPS ? sub * NCH * 512 : ch * 4096 + sub * (int)box);
         int st = 0, ph = 1, turn = 0, n = 0;  // stage, its empty parity (the first round passes), whose load, segments begun
         bool ok = true;
         for (;; ++n) {
@@ -447,8 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
         if (elect_one()) {
             constexpr uint32_t IDESC_QK = idesc_bf16(128, kKT, 0), IDESC_PV = idesc_bf16(128, D, 1);
             const uint64_t dq = smem_desc(smem_u32(sQ), 16, 512, kLayoutSwizzle64B);
-            const uint64_t dk = smem_desc(smem_u32(sKV), 16, 512, kLayoutSwizzle64B);
-            const uint64_t dv = smem_desc(smem_u32(sKV), 4096, 512, kLayoutSwizzle64B);
+            // bytes from a chunk to the next, and from eight keys to the next eight
+            constexpr uint32_t chunk = GROUPS ? 512 : 4096, group = GROUPS ? NCH * 512 : 512;
+            const uint64_t dk = smem_desc(smem_u32(sKV), 16, group, kLayoutSwizzle64B);
+            const uint64_t dv = smem_desc(smem_u32(sKV), chunk, group, kLayoutSwizzle64B);
             int seg = 0, st = 0;
             uint32_t ph = 0;                                         // the next stage in the order of use
             uint32_t nqk[2] = {0, 0}, npv[2] = {0, 0}, uses[2] = {0, 0};  // products and segments of each stream so far
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_bf16(tmem + 128 * s.value + 64 * b, dq + qt * (L::QTILE / 16) + ((ks >> 1) * 8192 + (ks & 1) * 32) / 16,
-                             dk + st * (L::TILE / 16) + ((ks >> 1) * 4096 + (ks & 1) * 32) / 16, IDESC_QK, ks > 0 ? 1u : 0u);
+                             dk + st * (L::TILE / 16) + (ks >> 1) * (chunk / 16) + (ks & 1) * 2, IDESC_QK, ks > 0 ? 1u : 0u);
                 mma_commit(s_full + 2 * s.value + b);
             };
             // O of stream s += P x V in the current stage; waits for P, and for O before its first use
@@ -481,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 #pragma unroll
                 for (int ks = 0; ks < kKT / 16; ++ks)
                     mma_bf16_ts(tmem + 256 + D * s.value, tmem + 128 * s.value + 64 * b + ks * 8,
-                                dv + st * (L::TILE / 16) + ks * 64, IDESC_PV, (!first || ks > 0) ? 1u : 0u);
+                                dv + st * (L::TILE / 16) + ks * (group / 8), IDESC_PV, (!first || ks > 0) ? 1u : 0u);
                 mma_commit(pv_done + s.value);
                 if (last) mma_commit(o_full + s.value);
                 return true;
@@ -605,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     // arrived, so the parity cannot be that of the stage's earlier round.
                     const int i = tile - ta, k = base + min(T, ahead) + i + min(i, max(T - ahead, 0)), st = k % ST;
                     if (!(ok = warp_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
-                    if (clean_values<NCH>(sKV + st * L::TILE, t, p1 + 1 - k0)) {
+                    if (clean_values<NCH, GROUPS>(sKV + st * L::TILE, t, p1 + 1 - k0)) {
                         s_bad[seg & 3] = seg + 1;
                         __threadfence_block();
                     }
@@ -814,15 +823,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-template <int D, int ST>
+template <int D, int ST, bool GROUPS>
 cudaError_t launch(const PagedMaps& tm, const PagedArgs& a, int grid, cudaStream_t st) {
     static PerDeviceOnce once;
     constexpr int smem = Lay<D, ST>::TOTAL + 512;
     cudaError_t e = per_device_once(once, [] {
-        return cudaFuncSetAttribute(paged_tc_kernel<D, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(paged_tc_kernel<D, ST, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
-    paged_tc_kernel<D, ST><<<grid, kThreads, smem, st>>>(tm, a);
+    paged_tc_kernel<D, ST, GROUPS><<<grid, kThreads, smem, st>>>(tm, a);
     ripe_count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -861,10 +870,11 @@ cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st) {
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const int rows = a.page < kKT ? a.page : kKT, chunks = rows == kKT ? a.d / 32 : 1;
+    const bool groups = a.page == 16;
+    const int rows = groups ? 8 : a.page < kKT ? a.page : kKT, chunks = groups || rows == kKT ? a.d / 32 : 1;
     if (!paged_kv_map(&tm.k, a.k, a, rows, chunks) || !paged_kv_map(&tm.v, a.v, a, rows, chunks)) return cudaErrorInvalidValue;
-    if (a.d == 64) return launch<64, 22>(tm, a, grid, st);
-    if (a.d == 96) return launch<96, 14>(tm, a, grid, st);
-    if (a.d == 128) return launch<128, 10>(tm, a, grid, st);
+    if (a.d == 64) return groups ? launch<64, 22, true>(tm, a, grid, st) : launch<64, 22, false>(tm, a, grid, st);
+    if (a.d == 96) return groups ? launch<96, 14, true>(tm, a, grid, st) : launch<96, 14, false>(tm, a, grid, st);
+    if (a.d == 128) return groups ? launch<128, 10, true>(tm, a, grid, st) : launch<128, 10, false>(tm, a, grid, st);
     return cudaErrorInvalidValue;
 }

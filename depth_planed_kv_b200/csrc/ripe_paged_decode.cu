@@ -4,14 +4,20 @@
 // The keys and values are read once and each feeds at most 16 rows, so the bytes are
 // what counts: a row tile of 128 in the tensor-memory kernel would be 7/8 empty, and
 // its pipeline's hand-overs cost more than the loads.  Here each warp streams its own
-// 16 keys of every 64-key tile through its own ring of stages (one TMA box for
-// the keys and one for the values; the warp that waits is the one that reuses the stage, so there is no other
-// hand-over) and keeps its own running maximum, sum and output in registers:
+// 16 keys of every 64-key tile through its own ring of stages (one TMA box for the keys
+// and one for the values; the warp that waits is the one that reuses the stage, so there
+// is no other hand-over) and keeps its own running maximum, sum and output in registers:
 //   S^T = K Q^T (keys on the 16-row side of m16n8k16, rows on its 8-column side),
 //   P^T by an 8x8 transpose in registers, O^T += V^T P^T.
 // The four warps of a CTA join at an item's end through shared memory; the running
 // maximum moves only when it grew by more than 2^8 (as in ripe_paged_sm100.cu), so most
 // blocks need no exchange between lanes at all.
+//
+// Measured with the merge: 16 sequences of 32768 keys, 32 query heads over 8, head size
+// 128, one token each: 343 us for 2.15 GB, 6.26 TB/s (a plain copy reaches 6.55).  One
+// sequence of 1024 keys and 55 heads of size 96: 14.3 us for 21.6 MB, bound by the chain of
+// latencies (plan, table, keys and values, join, then the merge kernel).  DRAM 78% and 18%
+// of peak.
 #include <cuda.h>
 #include <math.h>
 

@@ -29,6 +29,12 @@
 //     bin alone is gathered and sorted, and then all CTAs sum what is kept.
 //   else (many tokens in that bin, or a large k): bins of the ordered bit pattern inside
 //     the border's bin, until it holds one token or one value.
+//
+// Measured: 1 x 32000 fp32, all filters: 10.4 us, a chain of load, maximum, two cluster
+// barriers and one CTA's sort (clusters of 2 to 8 CTAs all take 10.5 to 11.4).  48 x 65537
+// bf16, top-p and min-p: 38 us (6 CTAs a row: 36, 4: 43, 2: 56), and 256 x 131072 fp32, all
+// filters: 148 us, 0.91 TB/s of 134 MB: instructions, 1.8 a cycle and SM; a token costs
+// about 220 in three passes (maximum; bin, weight and its atomics; what is kept).
 #include <math.h>
 
 #include "ripe_internal.cuh"

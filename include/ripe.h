@@ -381,12 +381,13 @@ int ripe_accept(int nseq, int k, int V, const float* zp, const float* zq, const 
  * them, while the mass before a token is below top_p times the mass of the first top_k;
  * of them, those with w_v >= min_p.  The first token is always kept.  The token drawn is
  * the smallest v whose running sum of kept w, in index order, exceeds u times the kept
- * mass (ripe_accept's draw).  A NaN logit counts as -inf; a row without any logit above
- * -inf gives token -1.
+ * mass (ripe_accept's draw).  A NaN logit counts as -inf, one of +inf as the largest
+ * finite value; a row without any logit above -inf gives token -1.
  * Outputs: token (device int32 [nrows]) and logprob (device float [nrows], or NULL): the
  * natural logarithm of the token's share of the kept mass (0 when greedy).
- * Weights are computed in 64 bits and summed exactly (in units of 2^-40 of the largest),
- * so the same inputs give the same token whatever the launch.
+ * Weights are integers of 2^-46 of the largest (2^-40 for V above 2^17), each right to
+ * about 2^-32 of itself, and summed exactly, so the same inputs give the same token
+ * whatever the launch.
  */
 int ripe_sample(int nrows, int V, const void* logits, int dtype, int64_t row_stride, const float* u,
                 const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token,

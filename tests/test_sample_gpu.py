@@ -1,8 +1,8 @@
 """The token draw (ripe_sample) against the fp64 oracle.  Tokens have to be equal: the
-kernel's sums are exact to 2^-41 of the largest weight per token, so a running sum and
-its border would have to lie within about 1e-9 of each other to disagree; rows closer
-than that are not drawn by these seeds (the test says so if one is).  logprob: one
-rounding to fp32 (2^-24 relative) of a value off by at most V * 2^-41: 1e-6 relative and
+kernel's weights are right to about 2^-32 of themselves and add up exactly, so a running
+sum and its border would have to lie within about 1e-9 of each other to disagree; rows
+closer than that are not drawn by these seeds (the test says so if one is).  logprob: a
+few roundings to fp32 (2^-24 relative) of a value off by about 2^-32: 1e-6 relative and
 1e-6 absolute cover it."""
 import numpy as np
 import pytest

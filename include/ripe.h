@@ -422,7 +422,8 @@ typedef struct {
  * ctx_len[i]+1, ...  table: int32 [nseq][table_width], row i at table + i*table_stride;
  * entries past a sequence's last page are not read.  All of it is read on the device,
  * so a call captured into a CUDA graph replays with new lengths and pages.  A sequence
- * whose offsets are wrong (RIPE_DEVERR_ROWS) or whose tokens do not fit its
+ * whose offsets are wrong (RIPE_DEVERR_ROWS; for the attention also one of more than
+ * max_ntok tokens) or whose tokens do not fit its
  * table_width*page <= 2^30 positions (RIPE_DEVERR_CAPACITY) is skipped: its rows are
  * left as they were, and so are rows that belong to no sequence.  err_dev (device int32,
  * or NULL) receives the first such condition, like a cache's device error word (a bounded

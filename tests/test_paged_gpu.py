@@ -294,3 +294,66 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for c, r in zip(cases, refs):
         assert np.abs(c.out[:c.rows].float().cpu().numpy() - r).max() < 0.05
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+def test_every_page_and_head_size_on_the_tensor_cores(page, d):
+    """Tiles of one page and of several, whole and cut by a sequence's end inside a page; the
+    slots behind it hold NaN."""
+    b = Batch([700, 1, 131], [50, 70, 200], 6, 2, d, page, seed=16, poison=float("nan"), token_major=page == 32)
+    b.check()
+    b.check(window=90, sinks=20)
+
+
+@pytest.mark.parametrize("case", [([9000], [6], 4, 2, 64, 16, "bf16"), ([9000], [60], 4, 2, 96, 16, "bf16"),
+                                  ([9000, 5000], [70, 90], 6, 2, 128, 64, "bf16"), ([3000], [6], 4, 2, 32, 16, "f32")], ids=str)
+def test_values_that_are_not_finite_in_an_item_cut_among_blocks(case):
+    """As the test above, with contexts long enough that several blocks share the item."""
+    b = Batch(*case, seed=17)
+    for ch, bad in ((5, float("inf")), (9, float("nan")), (30, -float("inf"))):
+        pos = b.ctx[0] + b.new[0] // 2
+        b.v[int(b.table[0, pos // b.page]), 1, pos % b.page, ch] = bad
+    got, lse = b.run()
+    ref, ref_lse = b.oracle()
+    assert np.abs(lse - ref_lse).max() < 2e-4
+    assert (np.isnan(got) == np.isnan(ref)).all() and (np.isposinf(got) == np.isposinf(ref)).all()
+    assert (np.isneginf(got) == np.isneginf(ref)).all()
+    ok = np.isfinite(ref)
+    assert not ok.all() and np.abs(got[ok] - ref[ok]).max() < 0.05
+
+
+@pytest.mark.parametrize("dtype,new", [("bf16", [1, 2]), ("bf16", [60, 40]), ("f32", [3, 30])])
+def test_pages_past_32_bit_offsets(dtype, new):
+    """Pages whose first element lies past 2^32 elements of the pool; keys and values in one
+    pool (the oracle gets the pages in use, renumbered)."""
+    from depth_planed_kv_b200.ripe import ripe_paged_append, ripe_paged_attn
+    npages, Hkv, page, d, H = 4200, 8, 1024, 128, 16
+    assert (npages - 10) * Hkv * page * d > 1 << 32
+    g = torch.Generator().manual_seed(18)
+    pool = torch.empty((npages, Hkv, page, d), dtype=DT[dtype], device="cuda")
+    ctx, used = [1500, 100], [npages - 1, npages - 3, npages - 4, 0]
+    for p in used:
+        pool[p] = torch.randn((Hkv, page, d), generator=g).to(DT[dtype]).cuda()
+    table = np.array([[used[0], used[3]], [used[2], used[1]]], np.int32)
+    small = np.array([[0, 3], [2, 1]])
+    row0 = np.array([0, new[0], sum(new)], np.int32)
+    kn, q = (torch.randn((sum(new), h, d), generator=g).to(DT[dtype]) for h in (Hkv, H))
+    O = torch.empty((sum(new), H, d), dtype=DT[dtype], device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.as_tensor(np.asarray(x, np.int32)).cuda()
+    ripe_paged_append(kn.cuda(), kn.cuda(), pool, pool, i32(table), i32(ctx), i32(row0), err=err)
+    ripe_paged_attn(q.cuda(), pool, pool, i32(table), i32(ctx), i32(row0), O, max_ntok=max(new), err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    few = torch.stack([pool[p] for p in used]).float().cpu().numpy()
+    row = kn.float().numpy()
+    for i in range(2):   # the write went where the table says
+        for j in range(new[i]):
+            pos = ctx[i] + j
+            assert (few[small[i, pos // page], :, pos % page] == row[row0[i] + j]).all()
+    ref, _ = PG.attn(q.float().numpy(), few, few, small, ctx, row0)
+    got = O.float().cpu().numpy()
+    vmax = np.abs(few).max()
+    tol = 2 ** -8 * np.abs(ref) + (2 ** -8 + 2 ** -12) * vmax if dtype == "bf16" else 2e-5 * vmax
+    assert (np.abs(got - ref) <= tol).all()

@@ -770,17 +770,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
 }
 
 // Joins the partials of an item that was cut, as paged_merge_kernel does, from this
-// kernel's slots: a warp takes eight rows, four lanes a row, and carries on maximum, sum
+// kernel's slots: a warp takes four rows, eight lanes a row, and carries on maximum, sum
 // and O from partial to partial (a partial's loads wait for nothing but the header).
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 4, kMergeRows = 4 * kMergeWarps;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_tc_merge_kernel(const __grid_constant__ PagedArgs a) {
     grid_dependency_wait();
     const int c1 = blockIdx.x;
     const PagedHdr h = a.hdr[c1];
-    const int lane = threadIdx.x % 32, piece = lane / 8;
-    const int row = (blockIdx.y * kMergeWarps + threadIdx.x / 32) * 8 + lane % 8;  // of the slot
+    const int lane = threadIdx.x % 32, piece = lane / 4;
+    const int row = blockIdx.y * kMergeRows + threadIdx.x / 32 * 4 + lane % 4;  // of the slot
     // the item's row: an M tile's rows past its last token are empty
     const int per = a.tok1 * a.G, i = row < 128 ? row : row - 128 + per;
     if (h.kind != 2 || (row & 127) >= per || i >= h.ntok * a.G) return;
@@ -790,9 +790,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_tc_merge_kernel(const 
     const float* rest = paged_slot(a, h.c0, 0);
     const int n = c1 - h.c0 + 1;
     float m = -INFINITY, l = 0.f;
-    float4 o[D / 16];
+    float4 o[D / 32];
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < D / 32; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
     for (int k = 0; k < n; ++k) {
         const float* p = k == 0 ? first : rest + k * stride;
@@ -802,8 +802,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_tc_merge_kernel(const 
         m = mn;
         l = l * f + lk * w;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            const float4 x = *reinterpret_cast<const float4*>(p + 2 * a.slot_rows + slot_at<D>(row, 16 * j + 4 * piece));
+        for (int j = 0; j < D / 32; ++j) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 2 * a.slot_rows + slot_at<D>(row, 32 * j + 4 * piece));
             o[j].x = o[j].x * f + x.x * w;
             o[j].y = o[j].y * f + x.y * w;
             o[j].z = o[j].z * f + x.z * w;
@@ -816,8 +816,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_tc_merge_kernel(const 
     const float inv = 1.f / l;
     char* dst = a.o + (orow * a.o_rs + (int64_t)head * D + 4 * piece) * 2;
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-        *reinterpret_cast<uint2*>(dst + 32 * j) =
+    for (int j = 0; j < D / 32; ++j)
+        *reinterpret_cast<uint2*>(dst + 64 * j) =
             make_uint2(pack_bf16(o[j].x * inv, o[j].y * inv), pack_bf16(o[j].z * inv, o[j].w * inv));
 }
 
@@ -847,7 +847,7 @@ cudaError_t launch(const PagedMaps& tm, const PagedArgs& a, int grid, cudaStream
     if (e != cudaSuccess) return e;
     // rows of the items: M tile 1 begins at slot row 128
     const int most = a.max_ntok <= a.tok1 ? a.max_ntok * a.G : 128 + (min(a.max_ntok, a.tpt) - a.tok1) * a.G;
-    return launch_paged_dependent(paged_tc_merge_kernel<D>, dim3((unsigned)grid, (unsigned)((most + 8 * kMergeWarps - 1) / (8 * kMergeWarps))),
+    return launch_paged_dependent(paged_tc_merge_kernel<D>, dim3((unsigned)grid, (unsigned)((most + kMergeRows - 1) / kMergeRows)),
                                   32 * kMergeWarps, st, a);
 }
 

@@ -28,8 +28,8 @@
 // the products need 1133 (64 columns a product: 49 cycles instead of 32, the queries'
 // reads from shared memory bind) and the exponential unit 1060; the softmax's serial parts
 // are the rest (two of its warps a scheduler, 46% of the issue slots used).  64 draft blocks of 8 tokens behind 512 to 4096, pages
-// of 16: 132 us for 654 MB, 5.0 TB/s: TMA issue and the items' ends.  2048 tokens alone,
-// 55 heads of size 96: 90 us, 0.49 PFLOP/s: items of 2 to 32 tiles, half of their time
+// of 16: 129 us for 654 MB, 5.1 TB/s: TMA issue and the items' ends.  2048 tokens alone,
+// 55 heads of size 96: 89 us, 0.50 PFLOP/s: items of 2 to 32 tiles, half of their time
 // their own beginnings and ends (the masked tiles, the last rows' way out).
 #include <cuda.h>
 #include <cudaTypedefs.h>

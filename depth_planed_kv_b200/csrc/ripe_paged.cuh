@@ -25,7 +25,9 @@ constexpr int kPagedMaxSeqs = 1024;
 // What a CTA left in its slot A: 0 nothing, 1 a middle stretch of an item, 2 the end
 // of an item (then the item follows).
 struct PagedHdr {
-    int kind, row0, ntok, head, c0, pad[3];  // c0: the CTA that began the item
+    int kind, row0, ntok, head, c0;  // c0: the CTA that began the item
+    int gaps;                        // CTAs between may have left nothing (kind 0)
+    int pad[2];
 };
 
 struct PagedArgs {
@@ -129,7 +131,7 @@ struct PagedSeg {
     int seq, c, r, n;       // the sequence (PagedSeq)
     int t0, ntok, head, w;  // the row tile's tokens, the key/value head, M tiles
     int ta, tb;
-    int c0;                 // the CTA that began the item, for a stretch that does not
+    int c0, gaps;           // the CTA that began the item, for a stretch that does not (PagedHdr)
     PagedTiles tiles;
 };
 
@@ -178,6 +180,7 @@ struct PagedPlan {
     int64_t stretch;   // its length, before the line's end cuts it
     int qt;            // row tile within the sequence
     int off;           // cost already behind x within the item
+    int cut;           // an item is cut at multiples of 2^cut key tiles
     PagedSeg s;        // the current item (s.head included)
 
     __device__ __forceinline__ int item(const PagedArgs& a) {  // s.seq, qt -> the row tile; its cost
@@ -195,10 +198,22 @@ struct PagedPlan {
         s.r = q.r;
     }
 
-    __device__ __forceinline__ void share(const PagedArgs& a, int64_t one_head, int min_cost) {
+    // A stretch shorter than min_cost is not worth its partials, so the CTAs take min_cost
+    // each, and not all work; or, with `pieces` and less than half of min_cost, items are cut
+    // into pieces of 2^pieces key tiles only, each taken whole by the CTA that its last key
+    // tile falls to, so that small items still spread over all CTAs.
+    __device__ __forceinline__ void share(const PagedArgs& a, int64_t one_head, int min_cost, int pieces) {
         const int64_t total = one_head * a.Hkv;
         int64_t len = paged_div(total + gridDim.x - 1, gridDim.x);
-        len = len < min_cost ? min_cost : len;
+        cut = 0;
+        if (len < min_cost) {
+            if (pieces > 0 && len * 2 < min_cost) {
+                cut = pieces;
+                len = len < 1 ? 1 : len;
+            } else {
+                len = min_cost;
+            }
+        }
         s.c0 = 0;
         stretch = len;
         x = len * blockIdx.x;
@@ -224,9 +239,10 @@ struct PagedPlan {
 
     // The thread that found the CTA's place tells the others.
     __device__ __forceinline__ void tell(PagedPlanHead& h) {
-        // The item begins where its first key tile's cost ends up: a CTA that ends inside that
-        // tile leaves it to the next.
-        s.c0 = (int)paged_div(x - off + s.w - 1, stretch);
+        // The item begins where its first piece's cost ends up: a CTA that ends inside that piece
+        // leaves it to the next.
+        s.c0 = (int)paged_div(x - off + (min(s.tiles.nt, 1 << cut) * s.w - 1), stretch);
+        s.gaps = cut > 0;
         h.s = s;
         h.qt = qt;
         h.off = off;
@@ -238,7 +254,7 @@ struct PagedPlan {
     // tile (about 4500 cycles each, where the way for any number takes 9000: 38 us against 36
     // for 23 single tokens beside a chunk of 509).
     template <int THREADS>
-    __device__ void begin(const PagedArgs& a, PagedPlanHead& h, PagedPlanSmem& sm, int min_cost) {
+    __device__ void begin(const PagedArgs& a, PagedPlanHead& h, PagedPlanSmem& sm, int min_cost, int pieces = 0) {
         static_assert(THREADS <= 1024, "one scan value per warp");
         const int tid = threadIdx.x;
         if (a.nseq <= THREADS && a.max_ntok <= 4 * a.tpt) {
@@ -255,7 +271,7 @@ struct PagedPlan {
             }
             int64_t total;
             const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
-            share(a, total, min_cost);
+            share(a, total, min_cost, pieces);
             if (x < x_end && (incl - cost) * a.Hkv <= x && x < incl * a.Hkv) {  // one thread's sequence
                 const int64_t y = head_of(a, incl - cost, cost);
                 qt = 0;
@@ -287,7 +303,7 @@ struct PagedPlan {
                 sm.tp[tid] = incl - cost;
                 if (tid == 0) sm.tp[THREADS] = total;
                 __syncthreads();
-                share(a, total, min_cost);
+                share(a, total, min_cost, pieces);
                 if (x < x_end && tid < base) {
                     const int64_t before = sm.tp[sm.sq[s.seq]], one = sm.tp[sm.sq[s.seq + 1]] - before;
                     if (before * a.Hkv <= x && x < (before + one) * a.Hkv) {  // in this sequence
@@ -326,7 +342,7 @@ struct PagedPlan {
                     sm.cp[i] = p;
                 }
                 __syncthreads();
-                share(a, total, min_cost);
+                share(a, total, min_cost, pieces);
                 if (x < x_end && tid == 0) {
                     int lo = 0, hi = a.nseq;  // the last sequence with cp * Hkv <= x: it has tiles
                     while (hi - lo > 1) {
@@ -390,8 +406,8 @@ struct PagedPlan {
             const int64_t room = x_end - x;
             const int end = (int)(room < c - off ? off + room : c);
             out = s;
-            out.ta = s.w == 2 ? off >> 1 : off;
-            out.tb = s.w == 2 ? end >> 1 : end;
+            out.ta = (off >> (s.w - 1)) & -(1 << cut);
+            out.tb = end == c ? s.tiles.nt : (end >> (s.w - 1)) & -(1 << cut);
             x += end - off;
             off = 0;
             if (++qt * (int64_t)a.tpt >= s.n) {

@@ -50,7 +50,11 @@ namespace {
 constexpr int kKT = 64;  // keys per tile
 constexpr int kThreads = 384;  // softmax warps 0-7 (4 a stream), the MMA warp, three TMA warps
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kTmaWarps = 3;
-constexpr int kMinCost = 8;    // key tiles x M tiles a CTA takes at least
+// Where there is less than kMinCost (key tiles x M tiles) a CTA, items are cut into pieces of
+// 2^kPieces key tiles.  (Stretches of 8 whatever the items: 4 sequences of 1 to 16 tokens
+// behind 19 took 34 us, one CTA all eight items; now 11.  Stretches of 1: 10, but 33 against 20
+// for one chunk of 673 tokens of one head, cut into halves of tiles; now 22.)
+constexpr int kMinCost = 8, kPieces = 2;
 
 struct alignas(64) PagedMaps {
     CUtensorMap q, k, v;
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
     if (warp == kTmaWarp && lane < 3) prefetch_tmap(lane == 0 ? &tm.q : lane == 1 ? &tm.k : &tm.v);
     PagedPlan<kKT> plan;  // carried on by the first TMA warp alone
     plan.template begin<kThreads>(a, *reinterpret_cast<PagedPlanHead*>(smem + L::PLAN), *reinterpret_cast<PagedPlanSmem*>(sKV),
-                                  kMinCost);
+                                  kMinCost, kPieces);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -656,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                 h.ntok = s.ntok;
                 h.head = s.head;
                 h.c0 = s.c0;
+                h.gaps = s.gaps;
                 a.hdr[blockIdx.x] = h;
             }
             const bool two = s.w == 1 && T > 1;  // both streams hold a part of the one M tile
@@ -783,18 +788,21 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_tc_merge_kernel(const 
     const int row = blockIdx.y * kMergeRows + threadIdx.x / 32 * 4 + lane % 4;  // of the slot
     // the item's row: an M tile's rows past its last token are empty
     const int per = a.tok1 * a.G, i = row < 128 ? row : row - 128 + per;
-    if (h.kind != 2 || (row & 127) >= per || i >= h.ntok * a.G) return;
+    if (h.kind != 2) return;
+    const int n = c1 - h.c0 + 1;
+    // of the first 32 CTAs, those that left something
+    unsigned some = 0;
+    if (h.gaps) some = __ballot_sync(0xffffffffu, lane < n && (lane == 0 || a.hdr[h.c0 + lane].kind != 0));
+    if ((row & 127) >= per || i >= h.ntok * a.G) return;
     const int64_t stride = 2 * (int64_t)a.slot_rows * (D + 2);
     // partial k: slot B of CTA c0, then slot A of c0 + 1 ... c1
     const float* first = paged_slot(a, h.c0, 1);
     const float* rest = paged_slot(a, h.c0, 0);
-    const int n = c1 - h.c0 + 1;
     float m = -INFINITY, l = 0.f;
     float4 o[D / 32];
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int k = 0; k < n; ++k) {
+    auto join = [&](int k) {
         const float* p = k == 0 ? first : rest + k * stride;
         const float mk = p[row], lk = p[a.slot_rows + row];
         const float mn = fmaxf(m, mk);
@@ -809,6 +817,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_tc_merge_kernel(const 
             o[j].z = o[j].z * f + x.z * w;
             o[j].w = o[j].w * f + x.w * w;
         }
+    };
+    if (h.gaps) {
+        while (some) {
+            const int k = __ffs(some) - 1;
+            some &= some - 1;
+            if (some) {  // two at a time, their loads together
+                const int k2 = __ffs(some) - 1;
+                some &= some - 1;
+                join(k);
+                join(k2);
+            } else {
+                join(k);
+            }
+        }
+        for (int k = 32; k < n; ++k)
+            if (a.hdr[h.c0 + k].kind != 0) join(k);
+    } else {
+#pragma unroll 2
+        for (int k = 0; k < n; ++k) join(k);
     }
     const int tok = i / a.G, head = h.head * a.G + i - tok * a.G;
     const int64_t orow = h.row0 + tok;

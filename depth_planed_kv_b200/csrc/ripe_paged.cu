@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // shared memory by cp.async as they lie in the cache; fp32 arithmetic (FFMA).  Eight
 // lanes share a row: four of the 32 scores each, then d/8 channels of O each.
 constexpr int kSimtThreads = 128, kRows = 16, kKT = 32;
-constexpr int kSimtMinCost = 2;
+constexpr int kSimtMinCost = 1;  // key tiles a CTA takes at least (2: 26 short sequences 27 us, 1: 17)
 
 template <typename Elem>
 __device__ __forceinline__ float4 load4(const char* p);

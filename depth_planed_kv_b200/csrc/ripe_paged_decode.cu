@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kKT = 16 * kWarps;  // keys per tile: 16 per warp
-constexpr int kMinCost = 2;       // key tiles a CTA takes at least
+constexpr int kMinCost = 1;       // key tiles a CTA takes at least (2: 5 short sequences 11 us, 1: 8)
 
 struct alignas(64) DecodeMaps {
     CUtensorMap k, v;

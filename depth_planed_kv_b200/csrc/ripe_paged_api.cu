@@ -83,9 +83,10 @@ int make_plan(const ripe_pages_t* p, int H, int max_ntok, Plan& q) {
         return ripe_fail(RIPE_ERR_INVALID_ARG, "H=%d is not a multiple of Hkv=%d in [1,256]", H, p->Hkv);
     if (max_ntok < 1) return ripe_fail(RIPE_ERR_INVALID_ARG, "max_ntok=%d < 1", max_ntok);
     q.G = H / p->Hkv;
-    const bool tc = fused_supported(p->dtype, p->d);
-    if (q.G > (tc ? 128 : 16))
-        return ripe_fail(RIPE_ERR_UNSUPPORTED, "%d query heads per key/value head: at most %d here", q.G, tc ? 128 : 16);
+    const bool many = fused_supported(p->dtype, p->d);  // heads per key/value head
+    const bool tc = many || (p->dtype == RIPE_BF16 && p->d == 32);
+    if (q.G > (many ? 128 : 16))
+        return ripe_fail(RIPE_ERR_UNSUPPORTED, "%d query heads per key/value head: at most %d here", q.G, many ? 128 : 16);
     const int sms = device_sm_count();
     if (sms < 1) return ripe_fail(RIPE_ERR_CUDA, "no current CUDA device");
     if (tc && (int64_t)max_ntok * q.G <= 16) {

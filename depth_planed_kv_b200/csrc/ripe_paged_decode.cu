@@ -1,5 +1,5 @@
 // ripe_paged_decode.cu -- ripe_paged_attn for few rows: at most 16 rows per key/value
-// head and sequence (single tokens, short draft blocks); bf16, head size 64, 96 or 128.
+// head and sequence (single tokens, short draft blocks); bf16, head size 32, 64, 96 or 128.
 //
 // The keys and values are read once and each feeds at most 16 rows, so the bytes are
 // what counts: a row tile of 128 in the tensor-memory kernel would be 7/8 empty, and
@@ -382,6 +382,7 @@ cudaError_t launch(const DecodeMaps& tm, const PagedArgs& a, int grid, cudaStrea
 
 template <int NR>
 cudaError_t launch_d(const DecodeMaps& tm, const PagedArgs& a, int grid, cudaStream_t st) {
+    if (a.d == 32) return launch<32, NR, 8>(tm, a, grid, st);
     if (a.d == 64) return launch<64, NR, 6>(tm, a, grid, st);
     if (a.d == 96) return launch<96, NR, 4>(tm, a, grid, st);
     if (a.d == 128) return launch<128, NR, 3>(tm, a, grid, st);

@@ -1,6 +1,6 @@
 // ripe_paged_sm100.cu -- ripe_paged_attn on the tensor cores: chunks of new tokens
 // (prompts, chunks of prompts, draft blocks with many rows) over a paged cache; bf16,
-// head size 64, 96 or 128.
+// head size 32, 64, 96 or 128.
 //
 // Per item (row tile of tokens x the query heads of one key/value head, see
 // ripe_paged.cuh): S = Q K^T and O += P V with the online softmax
@@ -910,6 +910,7 @@ cudaError_t launch_paged_tc(PagedArgs a, int grid, cudaStream_t st) {
     const bool groups = a.page == 16;
     const int rows = groups ? 8 : a.page < kKT ? a.page : kKT, chunks = groups || rows == kKT ? a.d / 32 : 1;
     if (!paged_kv_map(&tm.k, a.k, a, rows, chunks) || !paged_kv_map(&tm.v, a.v, a, rows, chunks)) return cudaErrorInvalidValue;
+    if (a.d == 32) return groups ? launch<32, 40, true>(tm, a, grid, st) : launch<32, 40, false>(tm, a, grid, st);
     if (a.d == 64) return groups ? launch<64, 22, true>(tm, a, grid, st) : launch<64, 22, false>(tm, a, grid, st);
     if (a.d == 96) return groups ? launch<96, 14, true>(tm, a, grid, st) : launch<96, 14, false>(tm, a, grid, st);
     if (a.d == 128) return groups ? launch<128, 10, true>(tm, a, grid, st) : launch<128, 10, false>(tm, a, grid, st);

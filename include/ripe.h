@@ -468,8 +468,8 @@ int ripe_paged_append(const ripe_pages_t* pages, const ripe_paged_batch_t* batch
  * What lies in slots past a sequence's last token, and in keys a token does not see, has
  * no influence, whatever it is (infinities and NaN included).  A page id out of range is
  * read as page 0 (RIPE_DEVERR_PAGE): that sequence's rows then mean nothing.
- * max_ntok*(H/Hkv) <= 16 takes a kernel made for few rows per key; with bf16 and d in
- * {64, 96, 128} more rows run on tcgen05; all else runs on CUDA cores.
+ * With bf16 and d in {32, 64, 96, 128}, max_ntok*(H/Hkv) <= 16 takes a kernel made for few
+ * rows per key, and more rows run on tcgen05; all else runs on CUDA cores.
  */
 int ripe_paged_attn_workspace(const ripe_pages_t* pages, int H, int max_ntok, size_t* bytes);
 int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, int H, const void* Q, int64_t q_stride,

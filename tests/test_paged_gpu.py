@@ -357,3 +357,13 @@ def test_pages_past_32_bit_offsets(dtype, new):
     vmax = np.abs(few).max()
     tol = 2 ** -8 * np.abs(ref) + (2 ** -8 + 2 ** -12) * vmax if dtype == "bf16" else 2e-5 * vmax
     assert (np.abs(got - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+def test_head_size_32_on_the_tensor_cores(page):
+    """Few rows, and many, whole and cut; the slots behind a sequence's end hold NaN."""
+    for ctx, new, H, Hkv in (([0, 15, 700, 64], [1, 1, 1, 1], 6, 2), ([900, 3], [3, 5], 3, 1), ([4000], [9], 16, 1),
+                             ([700, 1, 131], [50, 70, 200], 6, 2), ([9000], [60], 4, 4)):
+        b = Batch(ctx, new, H, Hkv, 32, page, seed=19, poison=float("nan"), token_major=page == 32)
+        b.check()
+        b.check(window=90, sinks=20)

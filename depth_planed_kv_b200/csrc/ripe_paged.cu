@@ -91,7 +91,10 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // ------------------------------------------------------------------ attention on CUDA cores
 // Items of 16 rows (tokens x heads of the group), 32 keys at a time, double-buffered in
 // shared memory by cp.async as they lie in the cache; fp32 arithmetic (FFMA).  Eight
-// lanes share a row: four of the 32 scores each, then d/8 channels of O each.
+// lanes share a row: four of the 32 scores each, then d/8 channels of O each.  Bound by the
+// latency of shared memory at few warps (0.5 to 0.9 instructions a cycle and SM), so as many
+// CTAs as fit: 55 single tokens behind 1900 to 3200, 64 heads over 32 of size 80, bf16: 1.94
+// ms (two CTAs an SM 4.04; 1.4 GB, 0.73 TB/s).  4 tokens behind 48, two heads of size 16: 10 us.
 constexpr int kSimtThreads = 128, kRows = 16, kKT = 32;
 constexpr int kSimtMinCost = 1;  // key tiles a CTA takes at least (2: 26 short sequences 27 us, 1: 17)
 
@@ -132,6 +135,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
         const int p0 = s.c + s.t0, p1 = p0 + s.ntok - 1, rows = s.ntok * a.G;
         const int tok = row / a.G, pos = p0 + tok;
         const bool valid = row < rows;
+        const bool live = tid / 32 * 4 < rows;  // the warp has rows; a single token leaves three idle
         __syncthreads();  // the previous item's tiles and Q are no longer read
         for (int i = tid; i < kRows * nv; i += kSimtThreads) {
             const int r = i / nv, v = i - r * nv, tk = r / a.G;
@@ -178,59 +182,61 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
             __syncthreads();
             const char* K = sKV + b * 2 * tile;
             const char* V = K + tile;
-            const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
-            float sc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int i = 0; i < n4; ++i) {
-                const float4 q = load4<Elem>(sQ + row * pitch + i * 4 * ES);
+            if (live) {
+                const bool part = !paged_all_seen(a, k0, kKT, p0, p1);
+                float sc[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < n4; ++i) {
+                    const float4 q = load4<Elem>(sQ + row * pitch + i * 4 * ES);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 k = load4<Elem>(K + (sub + 8 * j) * pitch + i * 4 * ES);
-                    sc[j] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, sc[j]))));
-                }
-            }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sc[j] = part && !paged_seen(a, k0 + sub + 8 * j, pos) ? -INFINITY : sc[j] * a.scale_log2;
-                mx = fmaxf(mx, sc[j]);
-            }
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            const float mn = fmaxf(m, mx), f = m == mn ? 1.f : exp2f(m - mn), ref = mn == -INFINITY ? 0.f : mn;
-            m = mn;
-            l *= f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                o[j].x *= f;
-                o[j].y *= f;
-                o[j].z *= f;
-                o[j].w *= f;
-                const float e = exp2f(sc[j] - ref);
-                l += e;
-                s_p[row][sub + 8 * j] = e;
-            }
-            __syncwarp();  // a row's eight lanes sit in one warp
-            auto add = [&](int key, auto partial) {
-                const float p = s_p[row][key];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (sub + 8 * j < n4) {
-                        const float4 v = load4<Elem>(V + key * pitch + (sub + 8 * j) * 4 * ES);
-                        // a hidden key's value may be anything: it must not meet the zero weight
-                        const bool skip = partial.value && p == 0.f;
-                        o[j].x = skip ? o[j].x : fmaf(p, v.x, o[j].x);
-                        o[j].y = skip ? o[j].y : fmaf(p, v.y, o[j].y);
-                        o[j].z = skip ? o[j].z : fmaf(p, v.z, o[j].z);
-                        o[j].w = skip ? o[j].w : fmaf(p, v.w, o[j].w);
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 k = load4<Elem>(K + (sub + 8 * j) * pitch + i * 4 * ES);
+                        sc[j] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, sc[j]))));
                     }
                 }
-            };
-            if (part) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sc[j] = part && !paged_seen(a, k0 + sub + 8 * j, pos) ? -INFINITY : sc[j] * a.scale_log2;
+                    mx = fmaxf(mx, sc[j]);
+                }
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                const float mn = fmaxf(m, mx), f = m == mn ? 1.f : exp2f(m - mn), ref = mn == -INFINITY ? 0.f : mn;
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o[j].x *= f;
+                    o[j].y *= f;
+                    o[j].z *= f;
+                    o[j].w *= f;
+                    const float e = exp2f(sc[j] - ref);
+                    l += e;
+                    s_p[row][sub + 8 * j] = e;
+                }
+                __syncwarp();  // a row's eight lanes sit in one warp
+                auto add = [&](int key, auto partial) {
+                    const float p = s_p[row][key];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (sub + 8 * j < n4) {
+                            const float4 v = load4<Elem>(V + key * pitch + (sub + 8 * j) * 4 * ES);
+                            // a hidden key's value may be anything: it must not meet the zero weight
+                            const bool skip = partial.value && p == 0.f;
+                            o[j].x = skip ? o[j].x : fmaf(p, v.x, o[j].x);
+                            o[j].y = skip ? o[j].y : fmaf(p, v.y, o[j].y);
+                            o[j].z = skip ? o[j].z : fmaf(p, v.z, o[j].z);
+                            o[j].w = skip ? o[j].w : fmaf(p, v.w, o[j].w);
+                        }
+                    }
+                };
+                if (part) {
 #pragma unroll 8
-                for (int key = 0; key < kKT; ++key) add(key, std::true_type());
-            } else {
+                    for (int key = 0; key < kKT; ++key) add(key, std::true_type());
+                } else {
 #pragma unroll 8
-                for (int key = 0; key < kKT; ++key) add(key, std::false_type());
+                    for (int key = 0; key < kKT; ++key) add(key, std::false_type());
+                }
             }
             __syncthreads();  // before the next load into this buffer
         }

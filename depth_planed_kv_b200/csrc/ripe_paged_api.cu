@@ -102,7 +102,7 @@ int make_plan(const ripe_pages_t* p, int H, int max_ntok, Plan& q) {
         q.tpt = 2 * q.tok1;
     } else {
         q.kind = Plan::SIMT;
-        q.grid = 2 * sms;
+        q.grid = (p->d * (p->dtype == RIPE_BF16 ? 2 : 4) <= 256 ? 4 : 2) * sms;  // what shared memory holds
         q.slot_rows = 16;
         q.tok1 = q.tpt = 16 / q.G;
     }

@@ -367,3 +367,16 @@ def test_head_size_32_on_the_tensor_cores(page):
         b = Batch(ctx, new, H, Hkv, 32, page, seed=19, poison=float("nan"), token_major=page == 32)
         b.check()
         b.check(window=90, sinks=20)
+
+
+@pytest.mark.parametrize("ctx,new,H", [([0], [130], 1), ([200], [20], 1), ([900], [260], 1), ([3000], [17], 2), ([6000], [40], 4),
+                                       ([9000, 3], [20, 20], 1), ([250] * 40, [17] * 40, 1), ([63, 64, 65, 255, 257], [20] * 5, 3)])
+def test_small_calls_cut_into_pieces(ctx, new, H):
+    """One key/value head: less than half a block's least share each, items of one piece and of
+    many, more blocks than a warp has lanes on one item; the same bits every time."""
+    b = Batch(ctx, new, H, 1, 128, 64, seed=20)
+    b.check()
+    b.check(window=200, sinks=70)
+    o1, l1 = b.run()
+    o2, l2 = b.run()
+    assert (o1 == o2).all() and (l1 == l2).all()

@@ -8,8 +8,8 @@
 // An item costs its key tiles times its M tiles.  All items of the call, in the
 // order (sequence, head, row tile), form one line of that cost, and each CTA takes an
 // equal stretch of it, whatever the mix of lengths: the lengths are on the device
-// only, so each CTA finds its own stretch from ctx_len and row0 (two block-wide
-// scans, about 2 us).  An item inside one stretch is finished by its CTA; one that
+// only, so each CTA finds its own stretch from ctx_len and row0 (block-wide scans,
+// about 2.5 us).  An item inside one stretch is finished by its CTA; one that
 // is cut leaves partials (m, l, unnormalised O) for paged_merge_kernel, at most two
 // per CTA: the item its stretch begins inside (slot A), and the one it ends inside
 // (slot B).  The order of the merge follows the CTA numbers, so results repeat bit

@@ -135,6 +135,32 @@ def launch_count() -> int:
     return int(_lib.ripe_launch_count())
 
 
+def _elsewhere(stream, device) -> bool:
+    return stream is not None and stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Device memory for a call on `stream` (None: the current one), taken on that stream:
+    the allocator orders a block's uses only within the stream it was taken on, so one of
+    the current stream's may still be in use there by an earlier call."""
+    if not _elsewhere(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _outputs(shape, dtypes, device, stream) -> list:
+    """The same for what the caller gets, who may still read it on the current stream when
+    the last reference goes."""
+    out = [_empty(shape, t, device, stream) for t in dtypes]
+    if _elsewhere(stream, device):
+        for t in out:
+            t.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def ripe_accept(zp: torch.Tensor, zq: torch.Tensor, zf: Optional[torch.Tensor], x1: torch.Tensor,
                 x2: Optional[torch.Tensor], u: torch.Tensor, temperature: float, stream=None):
     """LoopSpec acceptance of [nseq][k] draft positions.  zp, zq, zf: float32
@@ -144,7 +170,7 @@ def ripe_accept(zp: torch.Tensor, zq: torch.Tensor, zf: Optional[torch.Tensor], 
     for t in (zp, zq) + ((zf,) if zf is not None else ()):
         assert t.dtype == torch.float32 and t.is_contiguous() and t.shape == zp.shape
     assert x1.dtype == torch.int32 and u.dtype == torch.float32 and u.shape == (nseq, k, 3)
-    out = [torch.empty(nseq, dtype=torch.int32, device=zp.device) for _ in range(3)]
+    out = _outputs(nseq, [torch.int32] * 3, zp.device, stream)
     _check(_lib.ripe_accept(nseq, k, V, _ptr(zp), _ptr(zq), _ptr(zf), _ptr(x1), _ptr(x2), _ptr(u),
                             ctypes.c_float(temperature), _ptr(out[0]), _ptr(out[1]), _ptr(out[2]),
                             _stream(stream)), "ripe_accept")
@@ -183,11 +209,7 @@ def ripe_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[tor
         else:
             assert t.dtype == dt and t.shape == (n,) and t.is_contiguous() and t.device == dev
             ptrs.append(t.data_ptr())
-    token = torch.empty(n, dtype=torch.int32, device=dev)
-    logprob = torch.empty(n, dtype=torch.float32, device=dev)
-    if stream is not None:
-        token.record_stream(stream)
-        logprob.record_stream(stream)
+    token, logprob = _outputs(n, (torch.int32, torch.float32), dev, stream)
     _check(_lib.ripe_sample(n, V, logits.data_ptr(), _dtype_code(logits.dtype), logits.stride(0), *ptrs, token.data_ptr(),
                             logprob.data_ptr(), _raw_stream(stream, logits)), "ripe_sample")
     return token, logprob
@@ -278,7 +300,8 @@ def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor,
     """Attention of the batch's new tokens over the pages that hold them already.  Q, O:
     [nrows][H][d]; lse: float32 [nrows][H]; the batch as for ripe_paged_append.
     max_ntok: host bound on one sequence's new tokens (None: nrows; a decode batch gives
-    1).  work: device bytes (None: taken from torch's allocator for this call)."""
+    1).  work: device bytes (None: taken from torch's allocator for this call, on the call's
+    stream)."""
     pages = _pages(Kpages, Vpages)
     if not _here(Q):
         with torch.cuda.device(Kpages.device):
@@ -297,9 +320,7 @@ def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor,
         lp = lse.data_ptr()
     batch = _batch(table, ctx_len, row0, nrows, max_ntok, err, dev)
     if work is None:
-        work = torch.empty(_workspace(pages, Kpages, H, max_ntok), dtype=torch.uint8, device=dev)
-        if stream is not None:
-            work.record_stream(stream)
+        work = _empty(_workspace(pages, Kpages, H, max_ntok), torch.uint8, dev, stream)
     assert work.device == dev and work.is_contiguous()
     _check(_lib.ripe_paged_attn(pages, batch, H, Q.data_ptr(), qs, window, sinks, scale, O.data_ptr(), os_, lp,
                                 work.data_ptr(), work.nbytes, _raw_stream(stream, Q)), "ripe_paged_attn")

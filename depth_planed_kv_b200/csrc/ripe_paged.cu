@@ -18,7 +18,8 @@ namespace {
 // Row r of K and V goes to slot pos % page of page table[seq][pos / page], pos = ctx +
 // r - row0[seq].  A copy: bound by HBM (read once, written once).  One block per row and
 // share of its 16-byte vectors; the row's sequence comes from a 32-way search of row0
-// (two rounds of loads by one warp; 1024 sequences at most).  Three prompts of 1500 to 4000
+// (two rounds of loads by one warp; 1024 sequences at most), beside which the other warps
+// check that the offsets ascend, as the search takes them to.  Three prompts of 1500 to 4000
 // tokens, 55 heads of size 96: 47 us for 247 MB, 5.3 TB/s (a plain copy reaches 6.55); 64
 // ragged draft blocks: 3.4 us, a launch and three dependent loads.
 constexpr int kAppendThreads = 128, kAppendVecs = 4;
@@ -28,42 +29,55 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
                                                                       const char* __restrict__ V, int64_t row_stride,
                                                                       int esize) {
     const int64_t row = blockIdx.x;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     __shared__ int64_t s_off;  // elements from the pages' base to the token's head 0, or -1
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x, per = (a.nseq + 31) / 32;
-        // the last sequence with row0 <= row
-        const int i = min(lane * per, a.nseq);
-        const unsigned c = __ballot_sync(0xffffffffu, i < a.nseq && __ldg(a.row0 + i) <= row);
+    __shared__ int s_fall[kAppendThreads / 32 - 1];
+    // Where the row goes, by the last of the first n sequences with row0 <= row (warp 0).
+    auto place = [&](int n) {
+        const int per = (n + 31) / 32, i = min(lane * per, n);
+        const unsigned c = __ballot_sync(0xffffffffu, i < n && __ldg(a.row0 + i) <= row);
         const int lo = c ? (31 - __clz(c)) * per : 0;
         const int j = lo + lane;
-        const unsigned f = __ballot_sync(0xffffffffu, lane < per && j < a.nseq && __ldg(a.row0 + j) <= row);
+        const unsigned f = __ballot_sync(0xffffffffu, lane < per && j < n && __ldg(a.row0 + j) <= row);
         const int seq = f ? lo + 31 - __clz(f) : -1;
-        if (lane == 0) {
-            int64_t off = -1;
-            if (seq >= 0) {
-                const int r0 = __ldg(a.row0 + seq), e = __ldg(a.row0 + seq + 1), ctx = __ldg(a.ctx + seq);
-                if (r0 < 0 || e < r0 || e > a.nrows) {
-                    if (a.err) set_device_error(a.err, RIPE_DEVERR_ROWS);
-                } else if (row < e) {
-                    const int64_t pos = ctx + (row - r0);
-                    if (ctx < 0 || ctx + (int64_t)(e - r0) > (int64_t)a.table_width * a.page) {
-                        if (a.err) set_device_error(a.err, RIPE_DEVERR_CAPACITY);
-                    } else {
-                        const int id = __ldg(a.table + seq * a.table_stride + (pos >> a.page_shift));
-                        if (id < 0 || id >= a.npages) {
-                            if (a.err) set_device_error(a.err, RIPE_DEVERR_PAGE);
-                        } else {
-                            off = id * a.page_stride + (pos & (a.page - 1)) * a.pos_stride;
-                        }
-                    }
-                }
+        if (lane != 0) return;
+        int64_t off = -1;
+        if (seq >= 0) {
+            const PagedSeq q = paged_seq(a, seq, false);
+            if (row - q.r < q.n) {
+                const int64_t pos = q.c + (row - q.r);
+                const int id = __ldg(a.table + seq * a.table_stride + (pos >> a.page_shift));
+                off = (unsigned)id < (unsigned)a.npages ? id * a.page_stride + (pos & (a.page - 1)) * a.pos_stride : -2;
             }
-            s_off = off;
         }
+        s_off = off;
+    };
+    if (warp == 0) {
+        place(a.nseq);
+    } else {
+        // The other warps look for offsets that descend, and the first block's at every
+        // sequence: a bad one may own no row that a block would find it by.
+        const bool report = blockIdx.x == 0 && blockIdx.y == 0 && a.err;
+        int fall = a.nseq;
+        for (int i = threadIdx.x - 32; i < a.nseq; i += kAppendThreads - 32) {
+            if (__ldg(a.row0 + i + 1) < __ldg(a.row0 + i)) fall = min(fall, i);
+            if (report) paged_seq(a, i, true);
+        }
+        fall = __reduce_min_sync(0xffffffffu, fall);
+        if (lane == 0) s_fall[warp - 1] = fall;
     }
     __syncthreads();
+    int fall = s_fall[0];
+    for (int i = 1; i < kAppendThreads / 32 - 1; ++i) fall = min(fall, s_fall[i]);
+    if (fall < a.nseq) {  // the sequences from there on are skipped
+        if (warp == 0) place(fall);
+        __syncthreads();
+    }
     const int64_t off = s_off;
-    if (off < 0) return;
+    if (off < 0) {
+        if (off == -2 && threadIdx.x == 0 && a.err) set_device_error(a.err, RIPE_DEVERR_PAGE);
+        return;
+    }
     const int per_head = a.d * esize / 16, total = a.Hkv * per_head;
     const uint4* src[2] = {reinterpret_cast<const uint4*>(K + row * row_stride * esize),
                            reinterpret_cast<const uint4*>(V + row * row_stride * esize)};

@@ -50,9 +50,11 @@ struct PagedArgs {
 };
 
 // The chunk of sequence i: `n` tokens behind `c` cached ones, rows from `r`.  n = 0
-// for a sequence that is skipped (bad offsets, or past its pages).
+// for a sequence that is skipped (bad offsets, or past its pages).  falls: its offsets
+// descend; then those behind it are skipped too, so that no row belongs to two.
 struct PagedSeq {
     int c, n, r;
+    bool falls;
 };
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int i, bool report) {
@@ -61,6 +63,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int i, bool re
     s.c = __ldg(a.ctx + i);
     const int e = __ldg(a.row0 + i + 1);
     s.n = 0;
+    s.falls = e < s.r;
     if (s.r < 0 || e < s.r || e > a.nrows || e - s.r > a.max_ntok) {
         if (report) set_device_error(a.err, RIPE_DEVERR_ROWS);
     } else if (s.c < 0 || (int64_t)s.c + (e - s.r) > (int64_t)a.table_width * a.page) {
@@ -149,8 +152,9 @@ struct PagedPlanSmem {
 };
 
 // Inclusive block-wide scan of one value per thread (all threads call it; one barrier).
+// `flag` becomes whether it was set in any thread.
 template <int THREADS, typename T>
-__device__ __forceinline__ T paged_scan(T v, T* warp_sums, T& total) {
+__device__ __forceinline__ T paged_scan(T v, T* warp_sums, T& total, bool& flag) {
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -158,7 +162,7 @@ __device__ __forceinline__ T paged_scan(T v, T* warp_sums, T& total) {
         if (lane >= o) v += y;
     }
     if (lane == 31) warp_sums[w] = v;
-    __syncthreads();
+    flag = __syncthreads_or(flag);
     total = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
@@ -178,6 +182,7 @@ template <int KT>
 struct PagedPlan {
     int64_t x, x_end;  // this CTA's stretch of the line (x moves)
     int64_t stretch;   // its length, before the line's end cuts it
+    int nseq;          // sequences before the first whose offsets descend (while the plan is made)
     int qt;            // row tile within the sequence
     int off;           // cost already behind x within the item
     int cut;           // an item is cut at multiples of 2^cut key tiles
@@ -248,6 +253,18 @@ struct PagedPlan {
         h.off = off;
     }
 
+    // The least `i` of the block's threads, where offsets descend (seldom: barriers as needed).
+    __device__ __noinline__ static int first_fall(PagedPlanHead& h, int i) {
+        __syncthreads();
+        if (threadIdx.x == 0) h.qt = 0x7fffffff;
+        __syncthreads();
+        atomicMin(&h.qt, i);
+        __syncthreads();
+        const int least = h.qt;
+        __syncthreads();
+        return least;
+    }
+
     // All threads of the block; ends with a barrier, after which `sm` may be reused.  This
     // runs before anything else of the kernel, once and from a cold instruction cache, so the
     // usual cases have short ways of their own, few row tiles per sequence or a thread per row
@@ -257,6 +274,8 @@ struct PagedPlan {
     __device__ void begin(const PagedArgs& a, PagedPlanHead& h, PagedPlanSmem& sm, int min_cost, int pieces = 0) {
         static_assert(THREADS <= 1024, "one scan value per warp");
         const int tid = threadIdx.x;
+        bool falls = false;
+        nseq = a.nseq;
         if (a.nseq <= THREADS && a.max_ntok <= 4 * a.tpt) {
             // few row tiles per sequence: a thread per sequence, one scan
             s.n = 0;
@@ -267,10 +286,16 @@ struct PagedPlan {
                 s.c = q.c;
                 s.n = q.n;
                 s.r = q.r;
+                falls = q.falls;
                 for (qt = 0; qt * a.tpt < s.n; ++qt) cost += item(a);
             }
             int64_t total;
-            const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
+            const bool mine = falls;
+            int64_t incl = paged_scan<THREADS>(cost, h.warp, total, falls);
+            if (falls) {
+                if (tid >= first_fall(h, mine ? tid : 0x7fffffff)) cost = 0;
+                incl = paged_scan<THREADS>(cost, h.warp, total, falls);
+            }
             share(a, total, min_cost, pieces);
             if (x < x_end && (incl - cost) * a.Hkv <= x && x < incl * a.Hkv) {  // one thread's sequence
                 const int64_t y = head_of(a, incl - cost, cost);
@@ -280,18 +305,28 @@ struct PagedPlan {
             }
         } else {
             // row tiles before each sequence
-            int base = 0;
+            unsigned sum = 0;  // behind a sequence whose offsets descend it may be anything
+            int fall = 0x7fffffff;
             for (int i0 = 0; i0 < a.nseq; i0 += THREADS) {
                 const int i = i0 + tid;
-                int nq = 0, add;
-                if (i < a.nseq) nq = (paged_seq(a, i, blockIdx.x == 0).n + a.tpt - 1) / a.tpt;
-                const int incl = base + paged_scan<THREADS>(nq, reinterpret_cast<int*>(h.warp), add);
-                if (i < a.nseq) sm.sq[i + 1] = incl;
-                base += add;
+                unsigned nq = 0, add;
+                bool any = false;
+                if (i < a.nseq) {
+                    const PagedSeq q = paged_seq(a, i, blockIdx.x == 0);
+                    nq = (unsigned)((q.n + a.tpt - 1) / a.tpt);
+                    any = q.falls;
+                    if (any && fall == 0x7fffffff) fall = i;
+                }
+                const unsigned incl = sum + paged_scan<THREADS>(nq, reinterpret_cast<unsigned*>(h.warp), add, any);
+                if (i < a.nseq) sm.sq[i + 1] = (int)incl;
+                sum += add;
+                falls |= any;
                 __syncthreads();
             }
             if (tid == 0) sm.sq[0] = 0;
             __syncthreads();
+            if (falls) nseq = first_fall(h, fall);
+            const int base = falls ? sm.sq[nseq] : (int)sum;
             if (base <= THREADS) {
                 // a thread per row tile
                 int64_t cost = 0, total;
@@ -299,7 +334,7 @@ struct PagedPlan {
                     find(a, sm, tid);
                     cost = item(a);
                 }
-                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
+                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total, falls);
                 sm.tp[tid] = incl - cost;
                 if (tid == 0) sm.tp[THREADS] = total;
                 __syncthreads();
@@ -326,10 +361,10 @@ struct PagedPlan {
                         step(a);
                     }
                 }
-                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
+                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total, falls);
                 sm.tp[tid] = incl - cost;
                 __syncthreads();
-                for (int i = tid; i <= a.nseq; i += THREADS) {
+                for (int i = tid; i <= nseq; i += THREADS) {
                     const int q = sm.sq[i], run = q / per;
                     int64_t p = q < base ? sm.tp[run] : total;
                     if (q < base) {
@@ -344,7 +379,7 @@ struct PagedPlan {
                 __syncthreads();
                 share(a, total, min_cost, pieces);
                 if (x < x_end && tid == 0) {
-                    int lo = 0, hi = a.nseq;  // the last sequence with cp * Hkv <= x: it has tiles
+                    int lo = 0, hi = nseq;  // the last sequence with cp * Hkv <= x: it has tiles
                     while (hi - lo > 1) {
                         const int mid = (lo + hi) / 2;
                         if (sm.cp[mid] * a.Hkv <= x) lo = mid; else hi = mid;
@@ -376,7 +411,7 @@ struct PagedPlan {
     }
     // The sequence and row tile of global row tile q.
     __device__ __forceinline__ void find(const PagedArgs& a, const PagedPlanSmem& sm, int q) {
-        int lo = 0, hi = a.nseq;  // the last sequence with sq <= q has tiles: sq[lo + 1] > q
+        int lo = 0, hi = nseq;  // the last sequence with sq <= q has tiles: sq[lo + 1] > q
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (sm.sq[mid] <= q) lo = mid; else hi = mid;
@@ -389,13 +424,13 @@ struct PagedPlan {
         ++qt;
         if (qt * (int64_t)a.tpt >= s.n) {
             int i = s.seq + 1;
-            while (i < a.nseq) {
+            while (i < nseq) {
                 load(a, i);
                 if (s.n > 0) break;
                 ++i;
             }
             qt = 0;
-            if (i >= a.nseq) s.n = 0;
+            if (i >= nseq) s.n = 0;
         }
     }
 

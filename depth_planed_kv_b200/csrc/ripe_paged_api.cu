@@ -149,6 +149,7 @@ int ripe_paged_append(const ripe_pages_t* pages, const ripe_paged_batch_t* batch
     PagedArgs a;
     memset(&a, 0, sizeof a);
     fill(a, pages, batch);
+    a.max_ntok = batch->nrows;
     const cudaError_t e = launch_paged_append(a, (const char*)K, (const char*)V, row_stride, es, (cudaStream_t)stream);
     return e == cudaSuccess ? RIPE_OK : ripe_fail(RIPE_ERR_CUDA, "paged append launch: %s", cudaGetErrorString(e));
 }

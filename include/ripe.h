@@ -74,7 +74,8 @@ enum {
     RIPE_DEVERR_FORK = 7,        /* a fork pair with an id out of range, parent == child, or a parent
                                     that is itself a fork; that pair was skipped */
     RIPE_DEVERR_ROWS = 8,        /* a sequence's row offsets descend, leave [0, nrows] or hold more than
-                                    max_ntok tokens; that sequence was skipped */
+                                    max_ntok tokens; that sequence was skipped, and behind descending
+                                    offsets the others too */
     RIPE_DEVERR_PAGE = 9         /* a page id outside [0, npages): read as page 0, not written */
 };
 
@@ -425,7 +426,8 @@ typedef struct {
  * whose offsets are wrong (RIPE_DEVERR_ROWS; for the attention also one of more than
  * max_ntok tokens) or whose tokens do not fit its
  * table_width*page <= 2^30 positions (RIPE_DEVERR_CAPACITY) is skipped: its rows are
- * left as they were, and so are rows that belong to no sequence.  err_dev (device int32,
+ * left as they were, and so are rows that belong to no sequence.  Where a sequence's offsets
+ * descend, the ones behind it are skipped too: no row belongs to two.  err_dev (device int32,
  * or NULL) receives the first such condition, like a cache's device error word (a bounded
  * wait that ran out, RIPE_DEVERR_TIMEOUT, included: that call's outputs are incomplete).
  */

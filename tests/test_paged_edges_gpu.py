@@ -1,0 +1,119 @@
+"""Batches that a paged call has to sort out on the device: sequences that are skipped,
+and what that leaves of the others.  Tolerances as in test_paged_gpu.py (0.05 is several
+times them for these values, and far below what a wrong key does)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as PG
+from tests.test_paged_gpu import Batch
+
+pytestmark = pytest.mark.gpu
+
+
+def bad_batch(b, what):
+    """The batch's device arrays with sequence 1 spoilt; the code the calls report, and the
+    sequences that they still serve."""
+    table, ctx, row0 = b.dev()
+    last = (b.ctx[1] + b.new[1] - 1) // b.page
+    if what == "ctx":
+        ctx[1] = table.shape[1] * b.page - b.new[1] + 1
+    elif what == "neg":
+        ctx[1] = -1
+    elif what == "descend":   # sequence 2 would then claim a row of sequence 0
+        row0[2] = row0[1] - 1
+    elif what == "past":
+        row0[2:] = b.rows + 1
+    elif what == "negrow":
+        row0[0] = -1
+    elif what == "page":
+        table[1, last] = b.k.shape[0]
+    elif what == "negpage":
+        table[1, last] = -1
+    code = {"ctx": 2, "neg": 2, "descend": 8, "past": 8, "negrow": 8, "page": 9, "negpage": 9}[what]
+    good = {"ctx": [0, 2], "neg": [0, 2], "descend": [0], "past": [0], "negrow": [1, 2], "page": [0, 2], "negpage": [0, 2]}[what]
+    return (table, ctx, row0), code, good
+
+
+WHAT = ["ctx", "neg", "descend", "past", "negrow", "page", "negpage"]
+
+
+@pytest.mark.parametrize("what", WHAT)
+@pytest.mark.parametrize("new", [[2, 3, 1], [20, 60, 30]], ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_of_bad_sequences(dtype, new, what):
+    """The pages hold the served sequences' new tokens and are otherwise as before."""
+    from depth_planed_kv_b200.ripe import ripe_paged_append
+    b = Batch([20, 30, 40], new, 4, 2, 64, 16, dtype, seed=40)
+    dev, code, good = bad_batch(b, what)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((b.rows, 2, 64)).to(b.dtype).cuda() for _ in range(2))
+    rk, rv = b.k.cpu().float().numpy().copy(), b.v.cpu().float().numpy().copy()
+    kn, vn = k.float().cpu().numpy(), v.float().cpu().numpy()
+    for i in range(3):
+        for j in range(b.new[i]):
+            pos, r = b.ctx[i] + j, b.row0[i] + j
+            if i in good or (code == 9 and pos // b.page != (b.ctx[1] + b.new[1] - 1) // b.page):
+                rk[int(b.table[i, pos // b.page]), :, pos % b.page] = kn[r]
+                rv[int(b.table[i, pos // b.page]), :, pos % b.page] = vn[r]
+    ripe_paged_append(k, v, b.k, b.v, *dev, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == code
+    assert (b.k.float().cpu().numpy() == rk).all() and (b.v.float().cpu().numpy() == rv).all()
+
+
+@pytest.mark.parametrize("what", WHAT)
+@pytest.mark.parametrize("new,dtype", [([2, 3, 1], "bf16"), ([20, 60, 30], "bf16"), ([400, 300, 700], "bf16"),
+                                       ([2, 3, 1], "f32"), ([40, 60, 30], "f32")], ids=str)
+def test_attention_of_bad_sequences(new, dtype, what):
+    """The served sequences' rows are right; the skipped ones' are left as they were (a bad
+    page is read as page 0, so those rows mean nothing)."""
+    from depth_planed_kv_b200.ripe import ripe_paged_attn
+    b = Batch([20, 30, 40], new, 4, 2, 64, 16, dtype, seed=41)
+    ref, ref_lse = b.oracle()
+    dev, code, good = bad_batch(b, what)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ripe_paged_attn(b.q, b.k, b.v, *dev, b.out[:b.rows], b.lse[:b.rows], max_ntok=max(new), err=err)
+    torch.cuda.synchronize()
+    assert int(err) == code
+    o, lse = b.out.float().cpu().numpy(), b.lse.cpu().numpy()
+    for i in range(3):
+        r = slice(int(b.row0[i]), int(b.row0[i + 1]))
+        if i in good:
+            assert np.abs(o[r] - ref[r]).max() < 0.05 and np.abs(lse[r] - ref_lse[r]).max() < 2e-4
+        elif code != 9:
+            assert (o[r] == 77.0).all() and (lse[r] == 77.0).all()
+    assert (o[b.rows:] == 77.0).all()
+
+
+@pytest.mark.parametrize("nseq,at", [(3, 1), (200, 0), (200, 137), (1024, 600), (1024, 1023)])
+@pytest.mark.parametrize("most", [1, 40])
+def test_offsets_that_descend_among_many_sequences(nseq, at, most):
+    """All before the first such sequence is served, nothing from it on."""
+    from depth_planed_kv_b200.ripe import ripe_paged_append, ripe_paged_attn
+    rng = np.random.default_rng(nseq + at)
+    new = rng.integers(1, most + 1, nseq)
+    b = Batch(rng.integers(0, 40, nseq), new, 2, 1, 64, 16, seed=42)
+    table, ctx, row0 = b.dev()
+    row0[at + 1] = row0[at] - 1
+    if at + 4 < nseq:
+        row0[at + 3] = 0   # a second time, and rows of the first ones claimed once more
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kn = torch.randn((b.rows, 1, 64)).to(b.dtype).cuda()
+    rk, kf = b.k.float().cpu().numpy().copy(), kn.float().cpu().numpy()
+    for i in range(at):
+        for j in range(new[i]):
+            pos = b.ctx[i] + j
+            rk[int(b.table[i, pos // 16]), :, pos % 16] = kf[b.row0[i] + j]
+    ripe_paged_append(kn, kn, b.k, b.v, table, ctx, row0, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 8 and (b.k.float().cpu().numpy() == rk).all()
+    err.zero_()
+    ripe_paged_attn(b.q, b.k, b.v, table, ctx, row0, b.out[:b.rows], b.lse[:b.rows], max_ntok=most, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 8
+    ref, _ = b.oracle()
+    end = int(b.row0[at])
+    o = b.out.float().cpu().numpy()
+    assert end == 0 or np.abs(o[:end] - ref[:end]).max() < 0.05
+    assert (o[end:] == 77.0).all()

@@ -163,12 +163,13 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
         const int lr = tid / 4, lv = tid % 4;
         auto entry = [&](int t) {
             const int key = s.tiles.tile(t) * kKT + lr;
-            return t < s.tb && key <= p1 ? paged_entry(a, s.seq, key) : 0;
+            return t < s.tb && paged_any_seen(a, key, 1, p0, p1) ? paged_entry(a, s.seq, key) : 0;
         };
         int ent = entry(s.ta);
         auto load = [&](int t, int b) {
             const int key = s.tiles.tile(t) * kKT + lr;
-            const bool on = key <= p1;  // later slots hold anything: read as zeros
+            // Later slots hold anything, and behind the window the page may be gone: zeros.
+            const bool on = paged_any_seen(a, key, 1, p0, p1);
             const int64_t off = on ? (paged_checked(a, ent) * a.page_stride + s.head * a.head_stride +
                                       (key & (a.page - 1)) * a.pos_stride) * ES
                                    : 0;

@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             }
             const int ta = slot->ta, tb = slot->tb;
             if (ta == tb) break;
-            const int end = slot->c + slot->t0 + slot->ntok, head = slot->head, seq = slot->seq, slot_w = slot->w;
+            const int p0 = slot->c + slot->t0, end = p0 + slot->ntok, head = slot->head, seq = slot->seq, slot_w = slot->w;
             const PagedTiles tiles = slot->tiles;
             if (pw == 0) {
                 if (!(ok = warp_wait(q_free, (n & 1) ^ 1, abort_flag, a.err))) break;
@@ -422,14 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             // keys `ahead` tiles on.
             const int ahead = slot_w == 2 ? 2 : 4;
             auto on = [&](int t) { return t < tb && sub < nsub && tiles.tile(t) * kKT + sub * pb < end; };
-            auto entry = [&](int t) { return on(t) ? paged_entry(a, seq, tiles.tile(t) * kKT + sub * pb) : 0; };
+            // Behind the window a page may be gone, whatever the table says: a box that no row
+            // sees is read as zeros, by a page id past the last.
+            auto need = [&](int t) {
+                return on(t) && paged_any_seen(a, tiles.tile(t) * kKT + sub * pb, pb, p0, end - 1);
+            };
+            auto entry = [&](int t) { return need(t) ? paged_entry(a, seq, tiles.tile(t) * kKT + sub * pb) : 0; };
             auto load = [&](int t, int id, const CUtensorMap* map) {
                 const int k0 = tiles.tile(t) * kKT, y = (k0 + sub * pb) & (a.page - 1);
                 if (turn == pw) {
                     if (!warp_wait(kv_empty + st, ph, abort_flag, a.err)) return false;
                     if (lane == 0) mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
                     __syncwarp();
-                    if (on(t)) tma_load_5d(dst + st * L::TILE, map, 0, y, ch, head, paged_checked(a, id), kv_full + st);
+                    if (on(t))
+                        tma_load_5d(dst + st * L::TILE, map, 0, y, ch, head, need(t) ? paged_checked(a, id) : a.npages,
+                                    kv_full + st);
                     __syncwarp();
                 }
                 if (++turn == kTmaWarps) turn = 0;

@@ -468,8 +468,11 @@ int ripe_paged_append(const ripe_pages_t* pages, const ripe_paged_batch_t* batch
  *         for these sizes (RIPE_ERR_CAPACITY otherwise); need not be initialised.  Calls
  *         that may overlap on the GPU, replays of captured ones included, need one each.
  * What lies in slots past a sequence's last token, and in keys a token does not see, has
- * no influence, whatever it is (infinities and NaN included).  A page id out of range is
- * read as page 0 (RIPE_DEVERR_PAGE): that sequence's rows then mean nothing.
+ * no influence, whatever it is (infinities and NaN included).  Table entries of pages that
+ * none of a sequence's new tokens sees (behind the window and past the first `sinks`
+ * tokens) are not used: such pages may be given back, and the entries hold anything.  Any
+ * other page id out of range is read as page 0 (RIPE_DEVERR_PAGE): that sequence's rows
+ * then mean nothing.
  * With bf16 and d in {32, 64, 96, 128}, max_ntok*(H/Hkv) <= 16 takes a kernel made for few
  * rows per key, and more rows run on tcgen05; all else runs on CUDA cores.
  */

@@ -117,3 +117,47 @@ def test_offsets_that_descend_among_many_sequences(nseq, at, most):
     o = b.out.float().cpu().numpy()
     assert end == 0 or np.abs(o[:end] - ref[:end]).max() < 0.05
     assert (o[end:] == 77.0).all()
+
+
+RELEASED = [  # ctx, new, H, Hkv, d, dtype
+    ([700, 45, 1300], [1, 1, 1], 4, 2, 64, "bf16"),
+    ([700, 45, 1300], [3, 8, 2], 4, 2, 128, "bf16"),
+    ([700, 45, 1300], [40, 9, 200], 4, 2, 96, "bf16"),
+    ([700, 300, 1300], [400, 130, 20], 2, 2, 64, "bf16"),
+    ([2000], [33], 16, 1, 32, "bf16"),
+    ([700, 45, 1300], [1, 30, 2], 4, 2, 80, "bf16"),
+    ([700, 45, 600], [2, 1, 40], 4, 2, 64, "f32"),
+]
+
+
+@pytest.mark.parametrize("case", RELEASED, ids=str)
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 0), (70, 5), (33, 64), (250, 37)])
+def test_pages_behind_the_window_may_be_given_back(case, page, window, sinks):
+    """The table has no page any more where no token looks, and the pages that were there (and
+    page 0) hold NaN."""
+    from depth_planed_kv_b200.ripe import ripe_paged_attn
+    b = Batch(*case[:5], page, case[5], seed=43)
+    ref, ref_lse = b.oracle(window=window, sinks=sinks)
+    table, ctx, row0 = b.dev()
+    gone = []
+    for i, c in enumerate(b.ctx):
+        for p in range(table.shape[1]):
+            # all its positions behind the first new token's window, none among the first
+            if (p + 1) * page <= c + 1 - window and p * page >= sinks:
+                gone.append(int(b.table[i, p]))
+                table[i, p] = (-1, 1 << 30, -(1 << 31))[p % 3]
+    for x in (b.k, b.v):
+        if 0 in gone or 0 not in b.table:
+            x[0] = float("nan")
+        for p in gone:
+            x[p] = float("nan")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ripe_paged_attn(b.q, b.k, b.v, table, ctx, row0, b.out[:b.rows], b.lse[:b.rows], max_ntok=max(b.new), window=window,
+                    sinks=sinks, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0 and (gone or window > 100)
+    o, lse = b.out[:b.rows].float().cpu().numpy(), b.lse[:b.rows].cpu().numpy()
+    vmax = 6.0  # of that many normal deviates
+    tol = 2 ** -8 * np.abs(ref) + (2 ** -8 + 2 ** -12) * vmax if b.dtype == torch.bfloat16 else 2e-5 * vmax
+    assert (np.abs(o - ref) <= tol).all() and np.abs(lse - ref_lse).max() <= 2e-4

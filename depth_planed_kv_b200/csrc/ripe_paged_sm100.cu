@@ -143,12 +143,13 @@ __device__ __forceinline__ uint32_t zero_times(uint32_t w, uint32_t s) {
 }
 // Zeros the values the matrix product must not see in a key tile that some row sees
 // only in part: keys from `end` (of the tile) on, whose slots hold anything, and values
-// that are not finite (returns whether there were any; paged_nonfinite puts them back
+// that are not finite (`flag` then holds `mark`; paged_nonfinite puts them back
 // where they are seen).  128 threads, 16 bytes at a time in the order they lie.  With two
 // M tiles both streams clean the tile, each before its own product: what the later one
-// still writes is what the earlier one wrote.
+// still writes is what the earlier one wrote, and the flag is set before a value goes, so
+// that a stream which finds a value gone already finds the flag too.
 template <int NCH, bool GROUPS>
-__device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
+__device__ __forceinline__ void clean_values(char* sv, int t, int end, volatile int* flag, int mark) {
     if (end >= kKT) {
         // 0 * x adds up to 0 if x are all finite, else to NaN: an instruction a pair
         uint4 x[NCH * 2];
@@ -162,9 +163,8 @@ __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
             s0 = zero_times(x[i].z, s0);
             s1 = zero_times(x[i].w, s1);
         }
-        if ((s0 | s1) == 0) return false;
+        if ((s0 | s1) == 0) return;
     }
-    bool found = false;
 #pragma unroll 2
     for (int i = t; i < NCH * 256; i += 128) {
         uint4* at = reinterpret_cast<uint4*>(sv) + i;
@@ -181,11 +181,11 @@ __device__ __forceinline__ bool clean_values(char* sv, int t, int end) {
                 const uint32_t b = top(w);
                 return w & ~((b >> 15 & 1u) * 0x0000FFFFu | (b >> 31) * 0xFFFF0000u);
             };
+            *flag = mark;
+            __threadfence_block();
             *at = make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w));
-            found = true;
         }
     }
-    return found;
 }
 
 // One key tile of one row: S (64 columns, on their way into x and y) -> P over its first
@@ -635,10 +635,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     // arrived, so the parity cannot be that of the stage's earlier round.
                     const int i = tile - ta, k = base + min(T, ahead) + i + min(i, max(T - ahead, 0)), st = k % ST;
                     if (!(ok = warp_wait(kv_full + st, (k / ST) & 1, abort_flag, a.err))) break;
-                    if (clean_values<NCH, GROUPS>(sKV + st * L::TILE, t, p1 + 1 - k0)) {
-                        s_bad[seg & 3] = seg + 1;
-                        __threadfence_block();
-                    }
+                    clean_values<NCH, GROUPS>(sKV + st * L::TILE, t, p1 + 1 - k0, s_bad + (seg & 3), seg + 1);
+                    __threadfence_block();
                     fence_proxy_async_smem();
                     __syncwarp();
                     ok = softmax_step<D, true>(x, y, s_col + 64 * b, o_col, c2, pos - k0, a.window > 0 ? pos - a.window - k0 : -1,

@@ -161,3 +161,25 @@ def test_pages_behind_the_window_may_be_given_back(case, page, window, sinks):
     vmax = 6.0  # of that many normal deviates
     tol = 2 ** -8 * np.abs(ref) + (2 ** -8 + 2 ** -12) * vmax if b.dtype == torch.bfloat16 else 2e-5 * vmax
     assert (np.abs(o - ref) <= tol).all() and np.abs(lse - ref_lse).max() <= 2e-4
+
+
+@pytest.mark.parametrize("d,page", [(128, 64), (96, 32), (64, 16)])
+def test_both_row_tiles_of_an_item_know_of_values_that_are_not_finite(d, page):
+    """Two row tiles over the same key tiles, each of whose values is not finite somewhere:
+    whichever of the two softmax groups comes to a tile first, both give what the formula
+    gives, every time."""
+    from depth_planed_kv_b200.ripe import ripe_paged_attn
+    b = Batch([40, 333, 7], [256, 250, 200], 4, 2, d, page, seed=44)
+    for i in range(3):
+        for pos in range(b.ctx[i], b.ctx[i] + b.new[i], 29):   # channel by channel, seen by later rows
+            ch = pos * 5 % d
+            b.v[int(b.table[i, pos // page]), pos % 2, pos % page, ch] = (float("nan"), float("inf"), -float("inf"))[pos % 3]
+    ref, _ = b.oracle()
+    dev = b.dev()
+    ok = np.isfinite(ref)
+    assert not ok.all() and ok.any()
+    for _ in range(60):
+        ripe_paged_attn(b.q, b.k, b.v, *dev, b.out[:b.rows], b.lse[:b.rows], max_ntok=max(b.new))
+        got = b.out[:b.rows].float().cpu().numpy()
+        assert (np.isnan(got) == np.isnan(ref)).all() and (np.isposinf(got) == np.isposinf(ref)).all()
+        assert (np.isneginf(got) == np.isneginf(ref)).all() and np.abs(got[ok] - ref[ok]).max() < 0.05

@@ -11,10 +11,12 @@
 //
 // A draw is a comparison of running sums with a border, so the sums must not depend on
 // the order of additions, and a weight's error must be small against the borders of a
-// flat row, 1/V apart: weights are integers of 2^-46 of the largest (2^-40 above 2^17
-// tokens; a sum of V of them stays below 2^63), which add up exactly in any order, each
-// right to about 2^-32 of itself.  (With 32-bit exponentials and sums about one row in
-// 10^4 of 10^5 near-equal tokens would draw its neighbour.)
+// flat row, 1/V apart: weights are integers of 2^-46 of the largest (2^-(63 - ceil(log2 V))
+// above 2^17 tokens, so that a sum of V of them stays within 2^63), which add up exactly in
+// any order.  Each is right to 2^-30 of itself and half a unit; V half units are below
+// 2^-24 of the largest weight, u's own resolution, up to 2^20 tokens (2^-18 for 2^23).
+// (With 32-bit exponentials and sums about one row in 10^4 of 10^5 near-equal tokens would
+// draw its neighbour.)
 //
 // One cluster of 1 to 8 CTAs per row; each CTA holds a contiguous slice of the row in
 // shared memory, so the logits are read from memory once.
@@ -179,7 +181,8 @@ struct Row {
     // 2^bits * exp((x - m) / T), rounded.  t = (m - x) * c (the difference with its rounding
     // error, the product through fused operations), t = k / 512 + r; 2^-t = 2^(-k / 512) (1 - q),
     // q = 1 - 2^-r = r (ln2 - r (ln2^2 / 2 - r ln2^3 / 6)) for |r| < 2^-9.9: the next term is
-    // below 2^-46, q is held to 2^-32 and the table to 2^-32.
+    // below 2^-46, q is right to 2^-31 (its fp32 steps 2^-33, its rounding 2^-32) and the table
+    // to 2^-31.
     __device__ __forceinline__ u64 weight(float x) const {
         const float hi = m - x, bb = hi - m, lo = (m - (hi - bb)) - (x + bb);
         const float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves the rounded integer in the low bits
@@ -981,7 +984,8 @@ cudaError_t launch_sample(int nrows, int V, const void* z, int bf16, int64_t row
     a.min_p = min_p;
     a.token = token;
     a.logprob = logprob;
-    a.bits = V <= (1 << 17) ? 46 : 40;
+    a.bits = 46;
+    while (V > 1ll << (63 - a.bits)) --a.bits;
     int cluster = 1;
     while (cluster < kMaxCluster && V > cluster * 2048) cluster *= 2;
     a.per = ((V + cluster - 1) / cluster + 7) / 8 * 8;  // slices begin alike against 16 bytes

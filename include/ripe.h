@@ -386,9 +386,11 @@ int ripe_accept(int nseq, int k, int V, const float* zp, const float* zq, const 
  * finite value; a row without any logit above -inf gives token -1.
  * Outputs: token (device int32 [nrows]) and logprob (device float [nrows], or NULL): the
  * natural logarithm of the token's share of the kept mass (0 when greedy).
- * Weights are integers of 2^-46 of the largest (2^-40 for V above 2^17), each right to
- * about 2^-32 of itself, and summed exactly, so the same inputs give the same token
- * whatever the launch.
+ * Weights are integers of 2^-46 of the largest (2^-(63 - ceil(log2 V)) for V above 2^17),
+ * each right to 2^-30 of itself and half a unit, and summed exactly, so the same inputs
+ * give the same token whatever the launch.  A token below half a unit weighs nothing; V of
+ * those weigh at most V half units: 2^-30 of the largest at V = 2^17, 2^-24 (u's own
+ * resolution) at 2^20, 2^-18 at 2^23.
  */
 int ripe_sample(int nrows, int V, const void* logits, int dtype, int64_t row_stride, const float* u,
                 const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token,

@@ -14,6 +14,8 @@ using namespace sm100;
 
 namespace {
 
+__device__ int32_t g_error_word;
+
 // ------------------------------------------------------------------ append
 // Row r of K and V goes to slot pos % page of page table[seq][pos / page], pos = ctx +
 // r - row0[seq].  A copy: bound by HBM (read once, written once).  One block per row and
@@ -57,7 +59,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     } else {
         // The other warps look for offsets that descend, and the first block's at every
         // sequence: a bad one may own no row that a block would find it by.
-        const bool report = blockIdx.x == 0 && blockIdx.y == 0 && a.err;
+        const bool report = blockIdx.x == 0 && blockIdx.y == 0;
         int fall = a.nseq;
         for (int i = threadIdx.x - 32; i < a.nseq; i += kAppendThreads - 32) {
             if (__ldg(a.row0 + i + 1) < __ldg(a.row0 + i)) fall = min(fall, i);
@@ -75,7 +77,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     }
     const int64_t off = s_off;
     if (off < 0) {
-        if (off == -2 && threadIdx.x == 0 && a.err) set_device_error(a.err, RIPE_DEVERR_PAGE);
+        if (off == -2 && threadIdx.x == 0) set_device_error(a.err, RIPE_DEVERR_PAGE);
         return;
     }
     const int per_head = a.d * esize / 16, total = a.Hkv * per_head;
@@ -391,6 +393,22 @@ cudaError_t simt_t(const PagedArgs& a, int grid, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t paged_error_word(int32_t** word) {
+    static PerDeviceOnce once;
+    static int32_t* words[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = per_device_once(once, [dev] {
+        void* p = nullptr;
+        const cudaError_t found = cudaGetSymbolAddress(&p, g_error_word);
+        words[dev & 63] = (int32_t*)p;
+        return found;
+    });
+    *word = words[dev & 63];
+    return e;
+}
 
 cudaError_t launch_paged_simt(PagedArgs a, int dtype, int grid, cudaStream_t st) {
     return dtype == RIPE_F32 ? simt_t<float>(a, grid, st) : simt_t<__nv_bfloat16>(a, grid, st);

@@ -75,7 +75,7 @@ int check_rows(const void* x, int64_t stride, int64_t least, int es, const char*
 struct Plan {
     enum { DECODE, TC, SIMT } kind;
     int G, grid, tok1, tpt, slot_rows;
-    size_t hdr, bytes;
+    size_t bytes;
 };
 
 int make_plan(const ripe_pages_t* p, int H, int max_ntok, Plan& q) {
@@ -106,13 +106,12 @@ int make_plan(const ripe_pages_t* p, int H, int max_ntok, Plan& q) {
         q.slot_rows = 16;
         q.tok1 = q.tpt = 16 / q.G;
     }
-    q.hdr = 256;  // an error word of the library's own, for calls without err_dev
-    const size_t part = (q.hdr + (size_t)q.grid * sizeof(PagedHdr) + 255) / 256 * 256;
+    const size_t part = ((size_t)q.grid * sizeof(PagedHdr) + 255) / 256 * 256;
     q.bytes = part + (size_t)q.grid * 2 * q.slot_rows * (p->d + 2) * sizeof(float);
     return RIPE_OK;
 }
 
-void fill(PagedArgs& a, const ripe_pages_t* p, const ripe_paged_batch_t* b) {
+int fill(PagedArgs& a, const ripe_pages_t* p, const ripe_paged_batch_t* b) {
     a.k = (const char*)p->K;
     a.v = (const char*)p->V;
     a.page_stride = p->npages == 1 ? p->d : p->page_stride;
@@ -131,6 +130,8 @@ void fill(PagedArgs& a, const ripe_pages_t* p, const ripe_paged_batch_t* b) {
     for (a.page_shift = 4; (1 << a.page_shift) < p->page;) ++a.page_shift;
     a.npages = p->npages;
     a.err = b->err_dev;
+    const cudaError_t e = a.err ? cudaSuccess : paged_error_word(&a.err);
+    return e == cudaSuccess ? RIPE_OK : ripe_fail(RIPE_ERR_CUDA, "device error word: %s", cudaGetErrorString(e));
 }
 
 }  // namespace
@@ -148,7 +149,7 @@ int ripe_paged_append(const ripe_pages_t* pages, const ripe_paged_batch_t* batch
     if ((rc = check_rows(V, row_stride, least, es, "V")) != RIPE_OK) return rc;
     PagedArgs a;
     memset(&a, 0, sizeof a);
-    fill(a, pages, batch);
+    if ((rc = fill(a, pages, batch)) != RIPE_OK) return rc;
     a.max_ntok = batch->nrows;
     const cudaError_t e = launch_paged_append(a, (const char*)K, (const char*)V, row_stride, es, (cudaStream_t)stream);
     return e == cudaSuccess ? RIPE_OK : ripe_fail(RIPE_ERR_CUDA, "paged append launch: %s", cudaGetErrorString(e));
@@ -183,7 +184,7 @@ int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, 
     if (!aligned(work, 256)) return ripe_fail(RIPE_ERR_UNALIGNED, "work must be 256-byte aligned");
     PagedArgs a;
     memset(&a, 0, sizeof a);
-    fill(a, pages, batch);
+    if ((rc = fill(a, pages, batch)) != RIPE_OK) return rc;
     a.q = (const char*)Q;
     a.o = (char*)O;
     a.lse = lse;
@@ -200,8 +201,7 @@ int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, 
     a.slot_rows = q.slot_rows;
     a.scale_log2 = (scale == 0.f ? 1.0f / sqrtf((float)pages->d) : scale) * 1.4426950408889634f;
     char* w = (char*)work;
-    if (!a.err) a.err = (int32_t*)w;
-    a.hdr = (PagedHdr*)(w + q.hdr);
+    a.hdr = (PagedHdr*)w;
     a.part = (float*)(w + q.bytes - (size_t)q.grid * 2 * q.slot_rows * (pages->d + 2) * sizeof(float));
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = q.kind == Plan::DECODE ? launch_paged_decode(a, q.grid, st)
@@ -209,6 +209,17 @@ int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, 
                                            : launch_paged_simt(a, pages->dtype, q.grid, st);
     if (e == cudaSuccess && q.kind != Plan::TC) e = launch_paged_merge(a, pages->dtype, q.grid, st);
     return e == cudaSuccess ? RIPE_OK : ripe_fail(RIPE_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
+}
+
+int ripe_paged_get_device_error(int32_t* code_host, ripe_stream_t stream) {
+    if (!code_host) return ripe_fail(RIPE_ERR_INVALID_ARG, "code_host is NULL");
+    const cudaStream_t st = (cudaStream_t)stream;
+    int32_t* word = nullptr;
+    cudaError_t e = paged_error_word(&word);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(code_host, word, sizeof(int32_t), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(int32_t), st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    return e == cudaSuccess ? RIPE_OK : ripe_fail(RIPE_ERR_CUDA, "paged device error: %s", cudaGetErrorString(e));
 }
 
 }  // extern "C"

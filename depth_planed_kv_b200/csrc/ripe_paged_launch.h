@@ -6,6 +6,9 @@
 
 struct PagedArgs;
 
+// The current device's error word for calls without err_dev.
+cudaError_t paged_error_word(int32_t** word);
+
 // A tensor map of the pages at `base`: boxes of `rows` positions of one page and head and
 // `chunks` times 32 channels, 64-byte swizzle (false: the driver refused it).
 bool paged_kv_map(void* map, const void* base, const PagedArgs& a, int rows, int chunks);

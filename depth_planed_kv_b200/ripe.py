@@ -83,6 +83,7 @@ _sig("ripe_paged_append", [_B, _B, _P, _P, ctypes.c_int64, _P])
 _sig("ripe_paged_attn_workspace", [_B, _I, _I, ctypes.POINTER(ctypes.c_size_t)])
 _sig("ripe_paged_attn", [_B, _B, _I, _P, ctypes.c_int64, _I, _I, ctypes.c_float, _P, ctypes.c_int64, _P, _P,
                          ctypes.c_size_t, _P])
+_sig("ripe_paged_get_device_error", [_P, _P])
 _sig("ripe_cache_buffers", [_P] + [ctypes.POINTER(_P)] * 7)
 _sig("ripe_read_meta", [_P, _P, _P, _P, _P])
 _sig("ripe_get_device_error", [_P, _P, _P])
@@ -96,6 +97,7 @@ EXPORTED = ["ripe_cache_bytes", "ripe_cache_create", "ripe_cache_destroy", "ripe
             "ripe_synth_fill", "ripe_cache_verify_path", "ripe_cache_set_all_depths_kernel",
             "ripe_debug_stall_next_verify", "ripe_accept", "ripe_sample",
             "ripe_paged_append", "ripe_paged_attn_workspace", "ripe_paged_attn",
+            "ripe_paged_get_device_error",
             "ripe_cache_buffers", "ripe_read_meta", "ripe_get_device_error", "ripe_launch_count",
             "ripe_error_string", "ripe_last_error"]
 
@@ -258,7 +260,9 @@ def ripe_paged_append(K: torch.Tensor, V: torch.Tensor, Kpages: torch.Tensor, Vp
     """Write the new tokens' K and V ([nrows][Hkv][d], rows of any one stride) into the
     pages ([npages][Hkv][page][d], any strides): sequence i's rows row0[i]..row0[i+1]-1
     go behind its ctx_len[i] positions, through row i of the page table (int32
-    [nseq][width]).  err: device int32, see ripe.h."""
+    [nseq][width]).  err: device int32 that receives the code of what had to be skipped (a
+    sequence with bad offsets or past its pages, a bad page), as in ripe.h; None: the
+    device's own word, which ripe_paged_get_device_error reads."""
     pages = _pages(Kpages, Vpages)
     if not _here(K):
         with torch.cuda.device(Kpages.device):
@@ -300,7 +304,8 @@ def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor,
     """Attention of the batch's new tokens over the pages that hold them already.  Q, O:
     [nrows][H][d]; lse: float32 [nrows][H]; the batch as for ripe_paged_append.
     max_ntok: host bound on one sequence's new tokens (None: nrows; a decode batch gives
-    1).  work: device bytes (None: taken from torch's allocator for this call, on the call's
+    1); a sequence of more is skipped, its rows left as they were, and err says so (see
+    ripe_paged_append).  work: device bytes (None: taken from torch's allocator for this call, on the call's
     stream)."""
     pages = _pages(Kpages, Vpages)
     if not _here(Q):
@@ -324,6 +329,15 @@ def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor,
     assert work.device == dev and work.is_contiguous()
     _check(_lib.ripe_paged_attn(pages, batch, H, Q.data_ptr(), qs, window, sinks, scale, O.data_ptr(), os_, lp,
                                 work.data_ptr(), work.nbytes, _raw_stream(stream, Q)), "ripe_paged_attn")
+
+
+def ripe_paged_get_device_error(device=None, stream=None) -> int:
+    """Reads and clears the error word of calls without err on `device` (None: the current
+    one); waits for `stream` (None: the current one)."""
+    code = ctypes.c_int32()
+    with torch.cuda.device(device):
+        _check(_lib.ripe_paged_get_device_error(ctypes.byref(code), _stream(stream)), "ripe_paged_get_device_error")
+    return code.value
 
 
 def ripe_cache_bytes(layers, R, H, d, W, Tmax, max_seqs, kmax, dtype=torch.bfloat16) -> int:

@@ -430,7 +430,8 @@ typedef struct {
  * table_width*page <= 2^30 positions (RIPE_DEVERR_CAPACITY) is skipped: its rows are
  * left as they were, and so are rows that belong to no sequence.  Where a sequence's offsets
  * descend, the ones behind it are skipped too: no row belongs to two.  err_dev (device int32,
- * or NULL) receives the first such condition, like a cache's device error word (a bounded
+ * or NULL for a word of the device's own, read by ripe_paged_get_device_error) receives the
+ * first such condition, like a cache's device error word (a bounded
  * wait that ran out, RIPE_DEVERR_TIMEOUT, included: that call's outputs are incomplete).
  */
 typedef struct {
@@ -482,6 +483,10 @@ int ripe_paged_attn_workspace(const ripe_pages_t* pages, int H, int max_ntok, si
 int ripe_paged_attn(const ripe_pages_t* pages, const ripe_paged_batch_t* batch, int H, const void* Q, int64_t q_stride,
                     int window, int sinks, float scale, void* O, int64_t o_stride, float* lse, void* work,
                     size_t work_bytes, ripe_stream_t stream);
+
+/* Read and clear the current device's error word, which the two calls above share where
+ * their batch has no err_dev (synchronises stream; calls on other streams are not waited for). */
+int ripe_paged_get_device_error(int32_t* code_host, ripe_stream_t stream);
 
 /*
  * Test hook for the bounded-wait error path (the pages have no counterpart).  The

@@ -107,3 +107,7 @@ def test_binding_checks_shapes_before_the_call():
     with pytest.raises(AssertionError):   # host memory
         r._pages(k, k)
     assert r._PAGES.size == 72 and r._BATCH.size == 56
+
+
+def test_reading_the_devices_error_word_wants_a_place_for_it():
+    refused(lib()._lib.ripe_paged_get_device_error(None, None), INVALID)

@@ -183,3 +183,67 @@ def test_both_row_tiles_of_an_item_know_of_values_that_are_not_finite(d, page):
         got = b.out[:b.rows].float().cpu().numpy()
         assert (np.isnan(got) == np.isnan(ref)).all() and (np.isposinf(got) == np.isposinf(ref)).all()
         assert (np.isneginf(got) == np.isneginf(ref)).all() and np.abs(got[ok] - ref[ok]).max() < 0.05
+
+
+def test_calls_without_an_error_word_report_to_the_devices_own():
+    from depth_planed_kv_b200.ripe import ripe_paged_append, ripe_paged_attn, ripe_paged_get_device_error
+    b = Batch([20, 30, 40], [2, 3, 1], 4, 2, 64, 16, seed=45)
+    k = torch.randn((b.rows, 2, 64)).to(b.dtype).cuda()
+    table, ctx, row0 = b.dev()
+    assert ripe_paged_get_device_error() == 0
+    ripe_paged_append(k, k, b.k, b.v, table, ctx, row0)
+    ripe_paged_attn(b.q, b.k, b.v, table, ctx, row0, b.out[:b.rows], max_ntok=3)
+    assert ripe_paged_get_device_error() == 0
+    # a sequence longer than max_ntok: left as it was, and said so
+    b.out.fill_(77.0)
+    ripe_paged_attn(b.q, b.k, b.v, table, ctx, row0, b.out[:b.rows], max_ntok=2)
+    assert ripe_paged_get_device_error("cuda") == 8 and ripe_paged_get_device_error() == 0
+    assert bool((b.out[2:5] == 77.0).all()) and not bool((b.out[:2] == 77.0).any())
+    for what, code in (("ctx", 2), ("descend", 8), ("page", 9)):
+        dev, _, _ = bad_batch(b, what)
+        ripe_paged_append(k, k, b.k, b.v, *dev)
+        assert ripe_paged_get_device_error() == code
+        ripe_paged_attn(b.q, b.k, b.v, *dev, b.out[:b.rows], max_ntok=30)
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        assert ripe_paged_get_device_error(0, s) == code
+    # the caller's word keeps what it is told apart
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ripe_paged_append(k, k, b.k, b.v, *dev, err=err)
+    assert ripe_paged_get_device_error() == 0 and int(err) == 9
+
+
+FIRST_IN_CAPTURE = """
+import torch
+from depth_planed_kv_b200.ripe import ripe_paged_append, ripe_paged_attn, ripe_paged_get_device_error, ripe_sample
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+p = torch.randn((4, 2, 16, 64), device="cuda").bfloat16()
+k, q = torch.randn((3, 2, 64), device="cuda").bfloat16(), torch.randn((3, 4, 64), device="cuda").bfloat16()
+o = torch.zeros_like(q)
+table, ctx, row0 = i32([[1, 2], [3, 0]]), i32([14, 5]), i32([0, 2, 3])
+z, u = torch.randn((3, 5000), device="cuda"), torch.rand(3, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    ripe_paged_append(k, k, p, p, table, ctx, row0)
+    ripe_paged_attn(q, p, p, table, ctx, row0, o, max_ntok=2)
+    tok, _ = ripe_sample(z, u)
+g.replay()
+assert ripe_paged_get_device_error() == 0
+want = o.clone()
+ripe_paged_attn(q, p, p, table, ctx, row0, o, max_ntok=2)
+assert bool((o == want).all()) and bool((tok == ripe_sample(z, u)[0]).all())
+row0.copy_(i32([0, 3, 3]))   # three tokens where max_ntok says two
+g.replay()
+assert ripe_paged_get_device_error() == 8
+print("captured first")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]

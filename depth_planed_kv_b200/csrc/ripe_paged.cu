@@ -218,6 +218,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                 }
 #pragma unroll
                 for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                // Hidden keys get -0, so that the second product can leave them out: a weight that is 0
+                // because it is small still meets its value, as the formula has it.
                 const float mn = fmaxf(m, mx), f = m == mn ? 1.f : exp2f(m - mn), ref = mn == -INFINITY ? 0.f : mn;
                 m = mn;
                 l *= f;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                     o[j].w *= f;
                     const float e = exp2f(sc[j] - ref);
                     l += e;
-                    s_p[row][sub + 8 * j] = e;
+                    s_p[row][sub + 8 * j] = part && !paged_seen(a, k0 + sub + 8 * j, pos) ? -0.f : e;
                 }
                 __syncwarp();  // a row's eight lanes sit in one warp
                 auto add = [&](int key, auto partial) {
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                         if (sub + 8 * j < n4) {
                             const float4 v = load4<Elem>(V + key * pitch + (sub + 8 * j) * 4 * ES);
                             // a hidden key's value may be anything: it must not meet the zero weight
-                            const bool skip = partial.value && p == 0.f;
+                            const bool skip = partial.value && __float_as_uint(p) == 0x80000000u;
                             o[j].x = skip ? o[j].x : fmaf(p, v.x, o[j].x);
                             o[j].y = skip ? o[j].y : fmaf(p, v.y, o[j].y);
                             o[j].z = skip ? o[j].z : fmaf(p, v.z, o[j].z);

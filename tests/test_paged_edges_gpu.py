@@ -247,3 +247,24 @@ def test_the_first_calls_of_a_process_may_be_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("case", [([40], [6], 2, 2, 64, 16, "f32"), ([40], [6], 2, 2, 80, 32, "bf16"), ([40], [6], 2, 2, 64, 16, "bf16"),
+                                  ([40], [60], 2, 2, 64, 16, "bf16")], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_value_that_is_seen_counts_however_small_its_weight(case, bad):
+    """The weight of a key whose score is 300 below the largest is 0 in 32 bits; a NaN or
+    infinity it carries still makes the row one that is not finite, and no other row."""
+    from depth_planed_kv_b200.ripe import ripe_paged_attn
+    b = Batch(*case, seed=46)
+    pos = b.ctx[0] + 2
+    at = int(b.table[0, pos // b.page]), slice(None), pos % b.page
+    b.q[:] = 1.0
+    b.k[at] = -300.0 / b.d ** 0.5   # score -300, beside normal ones
+    b.v[at[0], :, at[2], 5] = bad
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ripe_paged_attn(b.q, b.k, b.v, *b.dev(), b.out[:b.rows], max_ntok=max(b.new), err=err)
+    o = b.out[:b.rows].float().cpu().numpy()
+    assert int(err) == 0
+    assert np.isfinite(o[:2]).all() and not np.isfinite(o[2:, :, 5]).any()
+    assert np.isfinite(np.delete(o, 5, axis=2)).all()

@@ -66,7 +66,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int i, bool re
     s.falls = e < s.r;
     if (s.r < 0 || e < s.r || e > a.nrows || e - s.r > a.max_ntok) {
         if (report) set_device_error(a.err, RIPE_DEVERR_ROWS);
-    } else if (s.c < 0 || (int64_t)s.c + (e - s.r) > (int64_t)a.table_width * a.page) {
+    } else if (e > s.r && (s.c < 0 || (int64_t)s.c + (e - s.r) > (int64_t)a.table_width * a.page)) {
         if (report) set_device_error(a.err, RIPE_DEVERR_CAPACITY);
     } else {
         s.n = e - s.r;

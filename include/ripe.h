@@ -421,18 +421,19 @@ typedef struct {
 /*
  * A batch of new tokens over pages, as the two calls below take it: sequence i of nseq
  * (0 <= nseq <= 1024) has ctx_len[i] cached positions and its new tokens are rows
- * row0[i] .. row0[i+1]-1 of the row arrays (none is allowed), at positions ctx_len[i],
- * ctx_len[i]+1, ...  table: int32 [nseq][table_width], row i at table + i*table_stride;
- * entries past a sequence's last page are not read.  All of it is read on the device,
- * so a call captured into a CUDA graph replays with new lengths and pages.  A sequence
- * whose offsets are wrong (RIPE_DEVERR_ROWS; for the attention also one of more than
- * max_ntok tokens) or whose tokens do not fit its
- * table_width*page <= 2^30 positions (RIPE_DEVERR_CAPACITY) is skipped: its rows are
- * left as they were, and so are rows that belong to no sequence.  Where a sequence's offsets
- * descend, the ones behind it are skipped too: no row belongs to two.  err_dev (device int32,
- * or NULL for a word of the device's own, read by ripe_paged_get_device_error) receives the
- * first such condition, like a cache's device error word (a bounded
- * wait that ran out, RIPE_DEVERR_TIMEOUT, included: that call's outputs are incomplete).
+ * row0[i] .. row0[i+1]-1 of the row arrays, at positions ctx_len[i], ctx_len[i]+1, ...;
+ * one may have none, as in a padded batch, and then its ctx_len and table hold anything.
+ * table: int32 [nseq][table_width], row i at table + i*table_stride; entries past a
+ * sequence's last page are not read.  All of it is read on the device, so a call captured
+ * into a CUDA graph replays with new lengths and pages.
+ * A sequence whose offsets are wrong (RIPE_DEVERR_ROWS; for the attention also one of more
+ * than max_ntok tokens) or whose tokens do not fit its table_width*page <= 2^30 positions
+ * (RIPE_DEVERR_CAPACITY) is skipped: its rows are left as they were, and so are rows that
+ * belong to no sequence.  Where a sequence's offsets descend, the ones behind it are skipped
+ * too: no row belongs to two.  err_dev (device int32, or NULL for a word of the device's
+ * own, read by ripe_paged_get_device_error) receives the first such condition, like a
+ * cache's device error word (a bounded wait that ran out, RIPE_DEVERR_TIMEOUT, included:
+ * that call's outputs are incomplete).
  */
 typedef struct {
     const int32_t* table;

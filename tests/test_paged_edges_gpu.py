@@ -268,3 +268,27 @@ def test_a_value_that_is_seen_counts_however_small_its_weight(case, bad):
     assert int(err) == 0
     assert np.isfinite(o[:2]).all() and not np.isfinite(o[2:, :, 5]).any()
     assert np.isfinite(np.delete(o, 5, axis=2)).all()
+
+
+@pytest.mark.parametrize("new,dtype", [([1, 0, 2, 0], "bf16"), ([40, 0, 60, 0], "bf16"), ([3, 0, 30, 0], "f32")], ids=str)
+@pytest.mark.parametrize("pad", [3, 500])
+def test_a_padded_batchs_empty_sequences_may_hold_anything(new, dtype, pad):
+    """Sequences without tokens, among the others and behind them, with lengths and pages that
+    mean nothing, are neither served nor reported."""
+    from depth_planed_kv_b200.ripe import ripe_paged_append, ripe_paged_attn
+    b = Batch([20, 30, 40, 9], new, 4, 2, 64, 16, dtype, seed=47)
+    ref, _ = b.oracle()
+    table = torch.cat([b.table, torch.full((pad, b.table.shape[1]), -9, dtype=torch.int32)])
+    table[1] = 1 << 30
+    ctx = [20, -1, 40, (1 << 31) - 1] + [(-1, 1 << 30, -(1 << 31))[i % 3] for i in range(pad)]
+    row0 = list(b.row0) + [b.rows] * pad
+    dev = [torch.as_tensor(np.asarray(x, np.int32)).cuda() for x in (table.numpy(), ctx, row0)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k0 = b.k.clone()
+    ripe_paged_attn(b.q, b.k, b.v, *dev, b.out[:b.rows], max_ntok=max(new), err=err)
+    k = torch.randn((b.rows, 2, 64)).to(b.dtype).cuda()
+    ripe_paged_append(k, k, b.k, b.v, *dev, err=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    assert np.abs(b.out[:b.rows].float().cpu().numpy() - ref).max() < 0.05
+    assert int((b.k != k0).any(-1).sum()) == b.rows * 2

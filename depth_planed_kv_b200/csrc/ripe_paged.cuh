@@ -144,6 +144,7 @@ struct PagedPlanHead {
     int64_t warp[32];
     PagedSeg s;  // where the CTA's stretch begins, as one thread finds it
     int qt, off;
+    int fall;               // the first sequence whose offsets descend
 };
 struct PagedPlanSmem {
     int64_t cp[kPagedMaxSeqs + 1];  // one head's cost before each sequence
@@ -152,9 +153,9 @@ struct PagedPlanSmem {
 };
 
 // Inclusive block-wide scan of one value per thread (all threads call it; one barrier).
-// `flag` becomes whether it was set in any thread.
+// *flag, if given, becomes whether it was set in any thread.
 template <int THREADS, typename T>
-__device__ __forceinline__ T paged_scan(T v, T* warp_sums, T& total, bool& flag) {
+__device__ __forceinline__ T paged_scan(T v, T* warp_sums, T& total, bool* flag = nullptr) {
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -162,7 +163,8 @@ __device__ __forceinline__ T paged_scan(T v, T* warp_sums, T& total, bool& flag)
         if (lane >= o) v += y;
     }
     if (lane == 31) warp_sums[w] = v;
-    flag = __syncthreads_or(flag);
+    if (flag) *flag = __syncthreads_or(*flag);
+    else __syncthreads();
     total = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
@@ -253,18 +255,6 @@ struct PagedPlan {
         h.off = off;
     }
 
-    // The least `i` of the block's threads, where offsets descend (seldom: barriers as needed).
-    __device__ __noinline__ static int first_fall(PagedPlanHead& h, int i) {
-        __syncthreads();
-        if (threadIdx.x == 0) h.qt = 0x7fffffff;
-        __syncthreads();
-        atomicMin(&h.qt, i);
-        __syncthreads();
-        const int least = h.qt;
-        __syncthreads();
-        return least;
-    }
-
     // All threads of the block; ends with a barrier, after which `sm` may be reused.  This
     // runs before anything else of the kernel, once and from a cold instruction cache, so the
     // usual cases have short ways of their own, few row tiles per sequence or a thread per row
@@ -275,6 +265,7 @@ struct PagedPlan {
         static_assert(THREADS <= 1024, "one scan value per warp");
         const int tid = threadIdx.x;
         bool falls = false;
+        if (tid == 0) h.fall = a.nseq;  // seen by the others behind a scan
         nseq = a.nseq;
         if (a.nseq <= THREADS && a.max_ntok <= 4 * a.tpt) {
             // few row tiles per sequence: a thread per sequence, one scan
@@ -291,10 +282,12 @@ struct PagedPlan {
             }
             int64_t total;
             const bool mine = falls;
-            int64_t incl = paged_scan<THREADS>(cost, h.warp, total, falls);
+            int64_t incl = paged_scan<THREADS>(cost, h.warp, total, &falls);
             if (falls) {
-                if (tid >= first_fall(h, mine ? tid : 0x7fffffff)) cost = 0;
-                incl = paged_scan<THREADS>(cost, h.warp, total, falls);
+                if (mine) atomicMin(&h.fall, tid);
+                __syncthreads();
+                if (tid >= h.fall) cost = 0;
+                incl = paged_scan<THREADS>(cost, h.warp, total);
             }
             share(a, total, min_cost, pieces);
             if (x < x_end && (incl - cost) * a.Hkv <= x && x < incl * a.Hkv) {  // one thread's sequence
@@ -306,27 +299,25 @@ struct PagedPlan {
         } else {
             // row tiles before each sequence
             unsigned sum = 0;  // behind a sequence whose offsets descend it may be anything
-            int fall = 0x7fffffff;
             for (int i0 = 0; i0 < a.nseq; i0 += THREADS) {
                 const int i = i0 + tid;
                 unsigned nq = 0, add;
-                bool any = false;
+                falls = false;
                 if (i < a.nseq) {
                     const PagedSeq q = paged_seq(a, i, blockIdx.x == 0);
                     nq = (unsigned)((q.n + a.tpt - 1) / a.tpt);
-                    any = q.falls;
-                    if (any && fall == 0x7fffffff) fall = i;
+                    falls = q.falls;
                 }
-                const unsigned incl = sum + paged_scan<THREADS>(nq, reinterpret_cast<unsigned*>(h.warp), add, any);
+                const unsigned incl = sum + paged_scan<THREADS>(nq, reinterpret_cast<unsigned*>(h.warp), add);
                 if (i < a.nseq) sm.sq[i + 1] = (int)incl;
+                if (falls) atomicMin(&h.fall, i);
                 sum += add;
-                falls |= any;
                 __syncthreads();
             }
             if (tid == 0) sm.sq[0] = 0;
             __syncthreads();
-            if (falls) nseq = first_fall(h, fall);
-            const int base = falls ? sm.sq[nseq] : (int)sum;
+            nseq = h.fall;
+            const int base = sm.sq[nseq];
             if (base <= THREADS) {
                 // a thread per row tile
                 int64_t cost = 0, total;
@@ -334,7 +325,7 @@ struct PagedPlan {
                     find(a, sm, tid);
                     cost = item(a);
                 }
-                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total, falls);
+                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
                 sm.tp[tid] = incl - cost;
                 if (tid == 0) sm.tp[THREADS] = total;
                 __syncthreads();
@@ -361,7 +352,7 @@ struct PagedPlan {
                         step(a);
                     }
                 }
-                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total, falls);
+                const int64_t incl = paged_scan<THREADS>(cost, h.warp, total);
                 sm.tp[tid] = incl - cost;
                 __syncthreads();
                 for (int i = tid; i <= nseq; i += THREADS) {

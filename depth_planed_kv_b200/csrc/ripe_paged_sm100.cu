@@ -424,10 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
             auto on = [&](int t) { return t < tb && sub < nsub && tiles.tile(t) * kKT + sub * pb < end; };
             // Behind the window a page may be gone, whatever the table says: a box that no row
             // sees is read as zeros, by a page id past the last.
-            auto need = [&](int t) {
-                return on(t) && paged_any_seen(a, tiles.tile(t) * kKT + sub * pb, pb, p0, end - 1);
+            const int gone_to = a.window > 0 ? p0 - a.window - pb + 1 : -1;  // paged_any_seen in two comparisons
+            auto gone = [&](int t) {
+                const int k = tiles.tile(t) * kKT + sub * pb;
+                return k <= gone_to && k >= a.sinks;
             };
-            auto entry = [&](int t) { return need(t) ? paged_entry(a, seq, tiles.tile(t) * kKT + sub * pb) : 0; };
+            auto entry = [&](int t) { return on(t) && !gone(t) ? paged_entry(a, seq, tiles.tile(t) * kKT + sub * pb) : 0; };
             auto load = [&](int t, int id, const CUtensorMap* map) {
                 const int k0 = tiles.tile(t) * kKT, y = (k0 + sub * pb) & (a.page - 1);
                 if (turn == pw) {
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tc_kernel(const __grid_cons
                     if (lane == 0) mbar_expect_tx(kv_full + st, min(nsub, (end - k0 + pb - 1) / pb) * NCH * box);
                     __syncwarp();
                     if (on(t))
-                        tma_load_5d(dst + st * L::TILE, map, 0, y, ch, head, need(t) ? paged_checked(a, id) : a.npages,
+                        tma_load_5d(dst + st * L::TILE, map, 0, y, ch, head, gone(t) ? a.npages : paged_checked(a, id),
                                     kv_full + st);
                     __syncwarp();
                 }

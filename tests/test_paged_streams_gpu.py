@@ -54,3 +54,29 @@ def test_draws_on_two_streams():
     for (tok, lp), out in held:
         assert (tok == want).all() and (lp == want_lp).all()
         assert all((t == w).all() for t, w in zip(out, acc))
+
+
+def test_a_side_stream_inside_a_captured_graph():
+    """The work space and the outputs of calls on a stream that joined the capture belong to
+    the graph."""
+    from depth_planed_kv_b200.ripe import ripe_paged_attn, ripe_sample
+    b = Batch([3000, 700], [70, 20], 8, 2, 128, 16, seed=33)
+    z, u = torch.randn((20, 9000), device="cuda"), torch.rand(20, device="cuda")
+    dev, s = b.dev(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        s.wait_stream(main)
+        ripe_paged_attn(b.q, b.k, b.v, *dev, b.out[:b.rows], max_ntok=70, stream=s)
+        tok, lp = ripe_sample(z, u, stream=s)
+        main.wait_stream(s)
+    ref, _ = b.oracle()
+    for _ in range(3):
+        b.out.fill_(77.0)
+        z.copy_(torch.randn(z.shape))
+        graph.replay()
+        eager, _ = ripe_sample(z, u)
+        other = torch.randn((1 << 20,), device="cuda")   # what is free is used by others meanwhile
+        torch.cuda.synchronize()
+        assert np.abs(b.out[:b.rows].float().cpu().numpy() - ref).max() < 0.05 and (tok == eager).all()
+        del other

@@ -163,15 +163,17 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
         }
         // Four threads a key; its page is looked up a tile ahead of its copies.
         const int lr = tid / 4, lv = tid % 4;
+        const int gone_to = a.window > 0 ? p0 - a.window : -1;
+        // Later slots hold anything, and behind the window the page may be gone: read as zeros.
+        auto needed = [&](int key) { return key <= p1 && (key > gone_to || key < a.sinks); };
         auto entry = [&](int t) {
             const int key = s.tiles.tile(t) * kKT + lr;
-            return t < s.tb && paged_any_seen(a, key, 1, p0, p1) ? paged_entry(a, s.seq, key) : 0;
+            return t < s.tb && needed(key) ? paged_entry(a, s.seq, key) : 0;
         };
         int ent = entry(s.ta);
         auto load = [&](int t, int b) {
             const int key = s.tiles.tile(t) * kKT + lr;
-            // Later slots hold anything, and behind the window the page may be gone: zeros.
-            const bool on = paged_any_seen(a, key, 1, p0, p1);
+            const bool on = needed(key);
             const int64_t off = on ? (paged_checked(a, ent) * a.page_stride + s.head * a.head_stride +
                                       (key & (a.page - 1)) * a.pos_stride) * ES
                                    : 0;
@@ -218,8 +220,6 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                 }
 #pragma unroll
                 for (int d = 1; d < 8; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                // Hidden keys get -0, so that the second product can leave them out: a weight that is 0
-                // because it is small still meets its value, as the formula has it.
                 const float mn = fmaxf(m, mx), f = m == mn ? 1.f : exp2f(m - mn), ref = mn == -INFINITY ? 0.f : mn;
                 m = mn;
                 l *= f;
@@ -231,7 +231,14 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const __grid_c
                     o[j].w *= f;
                     const float e = exp2f(sc[j] - ref);
                     l += e;
-                    s_p[row][sub + 8 * j] = part && !paged_seen(a, k0 + sub + 8 * j, pos) ? -0.f : e;
+                    s_p[row][sub + 8 * j] = e;
+                }
+                // Hidden keys get -0, so that the second product can leave them out: a weight that is 0
+                // because it is small still meets its value, as the formula has it.
+                if (part) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (!paged_seen(a, k0 + sub + 8 * j, pos)) s_p[row][sub + 8 * j] = -0.f;
                 }
                 __syncwarp();  // a row's eight lanes sit in one warp
                 auto add = [&](int key, auto partial) {

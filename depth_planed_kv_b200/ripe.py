@@ -138,14 +138,14 @@ def launch_count() -> int:
 
 
 def _elsewhere(stream, device) -> bool:
-    return stream is not None and stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """Device memory for a call on `stream` (None: the current one), taken on that stream:
     the allocator orders a block's uses only within the stream it was taken on, so one of
     the current stream's may still be in use there by an earlier call."""
-    if not _elsewhere(stream, device):
+    if stream is None or not _elsewhere(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
@@ -157,7 +157,7 @@ def _outputs(shape, dtypes, device, stream) -> list:
     """The same for what the caller gets, who may still read it on the current stream when
     the last reference goes."""
     out = [_empty(shape, t, device, stream) for t in dtypes]
-    if _elsewhere(stream, device):
+    if stream is not None and _elsewhere(stream, device):
         for t in out:
             t.record_stream(torch.cuda.current_stream(device))
     return out

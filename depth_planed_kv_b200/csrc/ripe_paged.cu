@@ -57,14 +57,26 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     if (warp == 0) {
         place(a.nseq);
     } else {
-        // The other warps look for offsets that descend, and the first block's at every
-        // sequence: a bad one may own no row that a block would find it by.
-        const bool report = blockIdx.x == 0 && blockIdx.y == 0;
+        // The other warps look for offsets that descend, and at the block's share of all
+        // sequences: a bad one may own no row that a block would find it by.
+        constexpr int kOthers = kAppendThreads - 32, kAhead = 4;
+        const int t = threadIdx.x - 32;
         int fall = a.nseq;
-        for (int i = threadIdx.x - 32; i < a.nseq; i += kAppendThreads - 32) {
-            if (__ldg(a.row0 + i + 1) < __ldg(a.row0 + i)) fall = min(fall, i);
-            if (report) paged_seq(a, i, true);
+        for (int i0 = t; i0 < a.nseq; i0 += kOthers * kAhead) {
+            int lo[kAhead], hi[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = min(i0 + j * kOthers, a.nseq - 1);
+                lo[j] = __ldg(a.row0 + i);
+                hi[j] = __ldg(a.row0 + i + 1);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (hi[j] < lo[j]) fall = min(fall, min(i0 + j * kOthers, a.nseq - 1));
         }
+        if (blockIdx.y == 0)
+            for (int64_t i = blockIdx.x + (int64_t)gridDim.x * t; i < a.nseq; i += (int64_t)gridDim.x * kOthers)
+                paged_seq(a, (int)i, true);
         fall = __reduce_min_sync(0xffffffffu, fall);
         if (lane == 0) s_fall[warp - 1] = fall;
     }

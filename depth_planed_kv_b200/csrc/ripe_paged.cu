@@ -23,7 +23,7 @@ __device__ int32_t g_error_word;
 // (two rounds of loads by one warp; 1024 sequences at most), beside which the other warps
 // check that the offsets ascend, as the search takes them to.  Three prompts of 1500 to 4000
 // tokens, 55 heads of size 96: 47 us for 247 MB, 5.3 TB/s (a plain copy reaches 6.55); 64
-// ragged draft blocks: 3.4 us, a launch and three dependent loads.
+// ragged draft blocks: 3.3 us, a launch and three dependent loads.
 constexpr int kAppendThreads = 128, kAppendVecs = 4;
 
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ PagedArgs a,
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // shared memory by cp.async as they lie in the cache; fp32 arithmetic (FFMA).  Eight
 // lanes share a row: four of the 32 scores each, then d/8 channels of O each.  Bound by the
 // latency of shared memory at few warps (0.5 to 0.9 instructions a cycle and SM), so as many
-// CTAs as fit: 55 single tokens behind 1900 to 3200, 64 heads over 32 of size 80, bf16: 1.94
-// ms (two CTAs an SM 4.04; 1.4 GB, 0.73 TB/s).  4 tokens behind 48, two heads of size 16: 10 us.
+// CTAs as fit: 55 single tokens behind 1900 to 3200, 64 heads over 32 of size 80, bf16: 1.97
+// ms (two CTAs an SM 4.04; 1.4 GB, 0.72 TB/s).  4 tokens behind 48, two heads of size 16: 10 us.
 constexpr int kSimtThreads = 128, kRows = 16, kKT = 32;
 constexpr int kSimtMinCost = 1;  // key tiles a CTA takes at least (2: 26 short sequences 27 us, 1: 17)
 

@@ -15,8 +15,8 @@
 //
 // Measured with the merge: 16 sequences of 32768 keys, 32 query heads over 8, head size
 // 128, one token each: 340 us for 2.15 GB, 6.3 TB/s (a plain copy reaches 6.55).  One
-// sequence of 1024 keys and 55 heads of size 96: 13.9 us for 21.6 MB, bound by the chain of
-// latencies (plan, table, keys and values, join, then the merge kernel).  DRAM 78% and 18%
+// sequence of 1024 keys and 55 heads of size 96: 14.0 us for 21.6 MB, bound by the chain of
+// latencies (plan, table, keys and values, join, then the merge kernel).  DRAM 77% and 17%
 // of peak.
 #include <cuda.h>
 #include <math.h>

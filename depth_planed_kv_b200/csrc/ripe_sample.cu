@@ -20,23 +20,28 @@
 //
 // One cluster of 1 to 8 CTAs per row; each CTA holds a contiguous slice of the row in
 // shared memory, so the logits are read from memory once.
-//   top-k up to a few hundred (the usual case): each CTA's threads have the largest logit
+//   top-k up to a few hundred: each CTA's threads have the largest logit
 //     of their share; the ceil(k / CTAs)-th largest of those is a bound that so many of the
 //     CTA's tokens reach, so the least such bound of the CTAs is reached by k tokens of the
-//     row, and by few more.  Those alone are gathered in the first CTA, sorted and drawn
-//     from; the other CTAs are done.
+//     row, and by few more where large logits lie all over the row.  Those alone are gathered
+//     in the first CTA, sorted and drawn from; the other CTAs are done.  Where they lie close
+//     together (rising or falling with the index, or a slice of -inf), the bound is too low, a
+//     CTA has more than its part of the list holds, and the row goes the last way below.
 //   top-p: 1024 bins of tokens and mass, linear in z below the maximum, which the CTAs
 //     read from one another through distributed shared memory, give the bin where the mass
 //     passes p.  The tokens down to it, if few, are gathered as above; else the border's
 //     bin alone is gathered and sorted, and then all CTAs sum what is kept.
-//   else (many tokens in that bin, or a large k): bins of the ordered bit pattern inside
+//   else (many tokens in that bin, a large k, or as above): bins of the ordered bit pattern inside
 //     the border's bin, until it holds one token or one value.
 //
-// Measured: 1 x 32000 fp32, all filters: 10.4 us, a chain of load, maximum, two cluster
-// barriers and one CTA's sort (clusters of 2 to 8 CTAs all take 10.5 to 11.4).  48 x 65537
-// bf16, top-p and min-p: 38 us (6 CTAs a row: 36, 4: 43, 2: 56), and 256 x 131072 fp32, all
-// filters: 148 us, 0.91 TB/s of 134 MB: instructions, 1.8 a cycle and SM; a token costs
-// about 220 in three passes (maximum; bin, weight and its atomics; what is kept).
+// Measured, normal logits: 1 x 32000 fp32, all filters: 10.7 us, a chain of load, maximum, two
+// cluster barriers and one CTA's sort (clusters of 2 to 8 CTAs all take 10.5 to 11.4).
+// 48 x 65537 bf16, top-p and min-p: 38 us (6 CTAs a row: 36, 4: 43, 2: 56).  256 x 131072
+// fp32, three rows in ten without top-k: 149 us, 0.90 TB/s of 134 MB.  Instructions bind the large ones; by the kind of row (256 x 131072, every row
+// alike), a warp's instructions for 32 tokens: top-k alone 36 (102 us), temperature alone 92
+// (160 us), top-p 165 (296 us: bin, weight and its atomics, the weight again for what is
+// kept), top-k with the large logits in one eighth of the row 145 (310 us; with top-p and
+// min-p besides 570, where they lie all over the row 102).
 #include <math.h>
 
 #include "ripe_internal.cuh"

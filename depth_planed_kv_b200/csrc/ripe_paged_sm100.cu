@@ -24,13 +24,14 @@
 //
 // Measured with the join of cut items: 2048 tokens behind 32768, 32 query heads over 8,
 // head size 128: 963 us after a rest, 1.18 PFLOP/s, and 1110 us in a long run under the power
-// cap, 1.02 PFLOP/s (cuBLAS 1.65 in a burst and near 1.4 under the cap).  A pair of 64-key tiles takes 1740 cycles there, where
-// the products need 1133 (64 columns a product: 49 cycles instead of 32, the queries'
-// reads from shared memory bind) and the exponential unit 1060; the softmax's serial parts
-// are the rest (two of its warps a scheduler, 46% of the issue slots used).  64 draft blocks of 8 tokens behind 512 to 4096, pages
-// of 16: 130 us for 654 MB, 5.0 TB/s (146 in a long run): TMA issue and the items' ends.
-// 2048 tokens alone, 55 heads of size 96: 91 us, 0.49 PFLOP/s: items of 2 to 32 tiles, half of their time
-// their own beginnings and ends (the masked tiles, the last rows' way out).
+// cap, 1.02 PFLOP/s (cuBLAS 1.65 in a burst and near 1.4 under the cap).  A pair of 64-key
+// tiles takes 1740 cycles there, where the products need 1133 (64 columns a product: 49
+// cycles instead of 32, the queries' reads from shared memory bind) and the exponential unit
+// 1060; the softmax's serial parts are the rest (two of its warps a scheduler, 46% of the
+// issue slots used).  64 draft blocks of 8 tokens behind 512 to 4096, pages of 16: 130 us
+// for 654 MB, 5.0 TB/s (146 in a long run): TMA issue and the items' ends.
+// 2048 tokens alone, 55 heads of size 96: 91 us, 0.49 PFLOP/s: items of 2 to 32 tiles, half
+// of their time their own beginnings and ends (the masked tiles, the last rows' way out).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>

@@ -31,17 +31,18 @@
 //     read from one another through distributed shared memory, give the bin where the mass
 //     passes p.  The tokens down to it, if few, are gathered as above; else the border's
 //     bin alone is gathered and sorted, and then all CTAs sum what is kept.
-//   else (many tokens in that bin, a large k, or as above): bins of the ordered bit pattern inside
+//   else (many tokens in that bin, a large k, or as above): bins of the ordered bit pattern in
 //     the border's bin, until it holds one token or one value.
 //
 // Measured, normal logits: 1 x 32000 fp32, all filters: 10.7 us, a chain of load, maximum, two
 // cluster barriers and one CTA's sort (clusters of 2 to 8 CTAs all take 10.5 to 11.4).
 // 48 x 65537 bf16, top-p and min-p: 38 us (6 CTAs a row: 36, 4: 43, 2: 56).  256 x 131072
-// fp32, three rows in ten without top-k: 149 us, 0.90 TB/s of 134 MB.  Instructions bind the large ones; by the kind of row (256 x 131072, every row
-// alike), a warp's instructions for 32 tokens: top-k alone 36 (102 us), temperature alone 92
-// (160 us), top-p 165 (296 us: bin, weight and its atomics, the weight again for what is
-// kept), top-k with the large logits in one eighth of the row 145 (310 us; with top-p and
-// min-p besides 570, where they lie all over the row 102).
+// fp32, three rows in ten without top-k: 149 us, 0.90 TB/s of 134 MB.  Instructions bind the
+// large ones; by the kind of row (256 x 131072, every row alike), a warp's instructions for 32
+// tokens: top-k alone 36 (102 us), temperature alone 92 (160 us), top-p 165 (296 us: bin,
+// weight and its atomics, the weight again for what is kept), top-k with the large logits in
+// one eighth of the row 145 (310 us; with top-p and min-p besides 570, where they lie all over
+// the row 102).
 #include <math.h>
 
 #include "ripe_internal.cuh"

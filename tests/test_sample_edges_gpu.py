@@ -53,3 +53,29 @@ def test_equal_logits_at_the_edges_of_the_weights_width(V):
         kept = V if "top_p" not in kw else int(np.ceil(float(np.float32(0.99999)) * V))
         at = [int(np.floor(float(x) * kept)) for x in u.cpu().numpy().astype(np.float64)]
         assert list(tok.cpu().numpy()) == at and np.allclose(lp.cpu().numpy(), -np.log(kept), atol=1e-5)
+
+
+@pytest.mark.parametrize("where", ["first eighth", "last eighth -inf", "middle", "falling", "rising"])
+@pytest.mark.parametrize("V,n,dtype", [(3000, 12, "f32"), (32000, 6, "f32"), (65537, 4, "bf16"), (131072, 3, "f32")])
+def test_large_logits_that_lie_together(V, n, dtype, where):
+    """Whatever part of the vocabulary the large logits are in, with and without the filters; no
+    margin of these seeds is below 1e-7, far above the weights' error."""
+    from tests.test_sample_gpu import check
+    rng = np.random.default_rng(V + len(where))
+    z = (rng.standard_normal((n, V)) * 3).astype(np.float32)
+    if where == "first eighth":
+        z[:, :V // 8] += 12
+    elif where == "last eighth -inf":
+        z[:, V - V // 8:] = -np.inf
+    elif where == "middle":
+        z[:, V // 2:V // 2 + 150] += 25
+    else:
+        z = np.sort(z, 1) if where == "rising" else -np.sort(-z, 1)
+    zd = torch.from_numpy(z).cuda()
+    zd = zd.bfloat16() if dtype == "bf16" else zd
+    one = np.ones(n, np.float32)
+    u = rng.random(n).astype(np.float32)
+    for k in (None, 3, 50, 200, 384, 1500):
+        ks = None if k is None else np.full(n, k, np.int32)
+        check(zd, u, one * np.float32(0.8), ks)
+        check(zd, u, one * np.float32(0.8), ks, one * np.float32(0.9), one * np.float32(0.02))

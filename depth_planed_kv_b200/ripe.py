@@ -305,8 +305,8 @@ def ripe_paged_attn(Q: torch.Tensor, Kpages: torch.Tensor, Vpages: torch.Tensor,
     [nrows][H][d]; lse: float32 [nrows][H]; the batch as for ripe_paged_append.
     max_ntok: host bound on one sequence's new tokens (None: nrows; a decode batch gives
     1); a sequence of more is skipped, its rows left as they were, and err says so (see
-    ripe_paged_append).  work: device bytes (None: taken from torch's allocator for this call, on the call's
-    stream)."""
+    ripe_paged_append).  work: device bytes (None: taken from torch's allocator for this
+    call, on the call's stream)."""
     pages = _pages(Kpages, Vpages)
     if not _here(Q):
         with torch.cuda.device(Kpages.device):

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         if (lane != 0) return;
         int64_t off = -1;
         if (seq >= 0) {
-            const PagedSeq q = paged_seq(a, seq, false);
+            const PagedSeq q = paged_seq(a, seq);
             if (row - q.r < q.n) {
                 const int64_t pos = q.c + (row - q.r);
                 const int id = __ldg(a.table + seq * a.table_stride + (pos >> a.page_shift));
@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         }
         s_off = off;
     };
+    int bad = 0, code = 0;
     if (warp == 0) {
         place(a.nseq);
     } else {
@@ -75,14 +76,17 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
                 if (hi[j] < lo[j]) fall = min(fall, min(i0 + j * kOthers, a.nseq - 1));
         }
         if (blockIdx.y == 0)
-            for (int64_t i = blockIdx.x + (int64_t)gridDim.x * t; i < a.nseq; i += (int64_t)gridDim.x * kOthers)
-                paged_seq(a, (int)i, true);
+            for (int64_t i = blockIdx.x + (int64_t)gridDim.x * t; i < a.nseq && code == 0; i += (int64_t)gridDim.x * kOthers) {
+                bad = (int)i;
+                code = paged_seq(a, bad).code;
+            }
         fall = __reduce_min_sync(0xffffffffu, fall);
         if (lane == 0) s_fall[warp - 1] = fall;
     }
     __syncthreads();
     int fall = s_fall[0];
     for (int i = 1; i < kAppendThreads / 32 - 1; ++i) fall = min(fall, s_fall[i]);
+    if (code && bad <= fall) set_device_error(a.err, code);
     if (fall < a.nseq) {  // the sequences from there on are skipped
         if (warp == 0) place(fall);
         __syncthreads();

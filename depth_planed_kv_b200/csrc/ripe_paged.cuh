@@ -50,24 +50,25 @@ struct PagedArgs {
 };
 
 // The chunk of sequence i: `n` tokens behind `c` cached ones, rows from `r`.  n = 0
-// for a sequence that is skipped (bad offsets, or past its pages).  falls: its offsets
-// descend; then those behind it are skipped too, so that no row belongs to two.
+// for a sequence that is skipped (bad offsets, or past its pages), code says why.  falls:
+// its offsets descend; then those behind it are skipped too, so that no row belongs to two,
+// and what code says of them means nothing.
 struct PagedSeq {
-    int c, n, r;
+    int c, n, r, code;
     bool falls;
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int i, bool report) {
+__device__ __forceinline__ PagedSeq paged_seq(const PagedArgs& a, int i) {
     PagedSeq s;
     s.r = __ldg(a.row0 + i);
     s.c = __ldg(a.ctx + i);
     const int e = __ldg(a.row0 + i + 1);
-    s.n = 0;
+    s.n = s.code = 0;
     s.falls = e < s.r;
     if (s.r < 0 || e < s.r || e > a.nrows || e - s.r > a.max_ntok) {
-        if (report) set_device_error(a.err, RIPE_DEVERR_ROWS);
+        s.code = RIPE_DEVERR_ROWS;
     } else if (e > s.r && (s.c < 0 || (int64_t)s.c + (e - s.r) > (int64_t)a.table_width * a.page)) {
-        if (report) set_device_error(a.err, RIPE_DEVERR_CAPACITY);
+        s.code = RIPE_DEVERR_CAPACITY;
     } else {
         s.n = e - s.r;
     }
@@ -198,7 +199,7 @@ struct PagedPlan {
         return s.tiles.nt * s.w;
     }
     __device__ __forceinline__ void load(const PagedArgs& a, int i) {
-        const PagedSeq q = paged_seq(a, i, false);
+        const PagedSeq q = paged_seq(a, i);
         s.seq = i;
         s.c = q.c;
         s.n = q.n;
@@ -271,13 +272,15 @@ struct PagedPlan {
             // few row tiles per sequence: a thread per sequence, one scan
             s.n = 0;
             int64_t cost = 0;
+            int code = 0;
             if (tid < a.nseq) {
-                const PagedSeq q = paged_seq(a, tid, blockIdx.x == 0);
+                const PagedSeq q = paged_seq(a, tid);
                 s.seq = tid;
                 s.c = q.c;
                 s.n = q.n;
                 s.r = q.r;
                 falls = q.falls;
+                code = q.code;
                 for (qt = 0; qt * a.tpt < s.n; ++qt) cost += item(a);
             }
             int64_t total;
@@ -287,8 +290,10 @@ struct PagedPlan {
                 if (mine) atomicMin(&h.fall, tid);
                 __syncthreads();
                 if (tid >= h.fall) cost = 0;
+                if (tid > h.fall) code = 0;
                 incl = paged_scan<THREADS>(cost, h.warp, total);
             }
+            if (code && blockIdx.x == 0) set_device_error(a.err, code);
             share(a, total, min_cost, pieces);
             if (x < x_end && (incl - cost) * a.Hkv <= x && x < incl * a.Hkv) {  // one thread's sequence
                 const int64_t y = head_of(a, incl - cost, cost);
@@ -299,12 +304,17 @@ struct PagedPlan {
         } else {
             // row tiles before each sequence
             unsigned sum = 0;  // behind a sequence whose offsets descend it may be anything
+            int bad = 0, code = 0;  // this thread's first sequence with a code
             for (int i0 = 0; i0 < a.nseq; i0 += THREADS) {
                 const int i = i0 + tid;
                 unsigned nq = 0, add;
                 falls = false;
                 if (i < a.nseq) {
-                    const PagedSeq q = paged_seq(a, i, blockIdx.x == 0);
+                    const PagedSeq q = paged_seq(a, i);
+                    if (code == 0) {
+                        bad = i;
+                        code = q.code;
+                    }
                     nq = (unsigned)((q.n + a.tpt - 1) / a.tpt);
                     falls = q.falls;
                 }
@@ -317,6 +327,7 @@ struct PagedPlan {
             if (tid == 0) sm.sq[0] = 0;
             __syncthreads();
             nseq = h.fall;
+            if (code && bad <= nseq && blockIdx.x == 0) set_device_error(a.err, code);
             const int base = sm.sq[nseq];
             if (base <= THREADS) {
                 // a thread per row tile

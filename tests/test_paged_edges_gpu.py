@@ -292,3 +292,26 @@ def test_a_padded_batchs_empty_sequences_may_hold_anything(new, dtype, pad):
     assert int(err) == 0
     assert np.abs(b.out[:b.rows].float().cpu().numpy() - ref).max() < 0.05
     assert int((b.k != k0).any(-1).sum()) == b.rows * 2
+
+
+@pytest.mark.parametrize("nseq,new", [(3, 20), (40, 1), (600, 3)])
+def test_descending_offsets_are_what_is_reported(nseq, new):
+    """Not what they make of the sequences behind them, here more tokens than the pages hold."""
+    from depth_planed_kv_b200.ripe import ripe_paged_append, ripe_paged_attn
+    b = Batch([20] * nseq, [new] * nseq, 4, 2, 64, 16, seed=48)
+    table, ctx, row0 = b.dev()
+    row0[2] = row0[1] - 1
+    row0[3:] = b.rows
+    if nseq > 3:
+        ctx[3:] = 1 << 29
+        row0[3] = 0
+    k = torch.randn((b.rows, 2, 64)).to(b.dtype).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(50):
+        for max_ntok in (1 << 20, 4):
+            ripe_paged_attn(b.q, b.k, b.v, table, ctx, row0, b.out[:b.rows], max_ntok=max(max_ntok, new), err=err)
+            assert int(err) == 8
+            err.zero_()
+        ripe_paged_append(k, k, b.k, b.v, table, ctx, row0, err=err)
+        assert int(err) == 8
+        err.zero_()

@@ -22,7 +22,7 @@ __device__ int32_t g_error_word;
 // share of its 16-byte vectors; the row's sequence comes from a 32-way search of row0
 // (two rounds of loads by one warp; 1024 sequences at most), beside which the other warps
 // check that the offsets ascend, as the search takes them to.  Three prompts of 1500 to 4000
-// tokens, 55 heads of size 96: 47 us for 247 MB, 5.3 TB/s (a plain copy reaches 6.55); 64
+// tokens, 55 heads of size 96: 46 us for 247 MB, 5.4 TB/s (a plain copy reaches 6.55); 64
 // ragged draft blocks: 3.3 us, a launch and three dependent loads.
 constexpr int kAppendThreads = 128, kAppendVecs = 4;
 
